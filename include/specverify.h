@@ -16,6 +16,10 @@
  *   mla_wuv_project     the per-head W_UV value up-projection after the merge.
  *   mla_kv_append       the verify tokens' latent rows into the paged cache.
  *   spec_verify_sampled rejection-sampling verification (probabilistic drafts).
+ *   kv_pages_copy       pages of one pool into pages of another or the same.
+ *   kv_pages_fork       requests continued from another's cache, sharing pages.
+ *   kv_pages_resize     the pages of new lengths, handed out and taken back.
+ *   kv_pages_compact    the pages in use moved to the front of the pool.
  *   spec_verify_greedy  target argmax, accepted draft prefix, next token and
  *                       trimmed per-request KV length.
  *
@@ -65,6 +69,11 @@ typedef enum {
 /* only in the index-checking debug build (compiled with -DSPECVERIFY_DEBUG):
  * an index or address check failed and its access was skipped */
 #define SV_DEV_DEBUG_CHECK 0x8
+
+/* page bookkeeping (kv_pages_*) */
+#define SV_DEV_SHARED_PAGE 0x10 /* a request would grow inside a page that others hold too */
+#define SV_DEV_NO_PAGE     0x20 /* the pool has too few free pages                         */
+#define SV_DEV_BAD_REQUEST 0x40 /* a request index out of range, or a child that is in use */
 
 #define SV_LATENT_DIM 512
 #define SV_PAGE_SIZE 64
@@ -295,6 +304,110 @@ sv_status mla_wuv_project(const void* x, const void* w_uv, int T, int H, int v_d
 sv_status mla_kv_append(const void* kv_new, const int32_t* positions, const int32_t* block_table,
                         int R, int q_per_req, int max_pages_per_req, void* kv_pages,
                         int num_pages, int page_size, int32_t* status, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The pages of the paged cache: kv_pages_copy, kv_pages_fork,
+ * kv_pages_resize, kv_pages_compact
+ *
+ * State, all of it the caller's device memory:
+ *   ref_counts   int32 [num_pages]: how many table entries hold the page.  A
+ *                page is free exactly when its count is 0; there is no other
+ *                allocator state, so a pool starts with all counts 0.
+ *   block_table  int32 [R][max_pages_per_req], as the attention reads it.
+ *   kv_lens      int32 [R]: request r holds the first ceil(kv_lens[r] / 64)
+ *                entries of its row; the others mean nothing.
+ *   kv_pages     [layers][num_pages][64][row_bytes], 16-byte aligned: the
+ *                pools of all layers that share the table (layers = 1 for one
+ *                pool).  row_bytes is 1024 for bf16 latent rows and 512 for
+ *                E4M3 codes; any multiple of 16 up to 2^24 is taken.
+ * Pages are handed out lowest free page first, in the order of the requests
+ * (fork: of the forks), so every result is a function of the inputs alone.
+ *
+ * ref_counts, block_table and kv_lens are read from the *_in arrays and the
+ * state after the call is written to the *_out arrays, whole; an *_out pointer
+ * may be the *_in pointer (update in place), other overlaps are not allowed.
+ * page_size must be 64.  R * max_pages_per_req and max_pages_per_req * 64
+ * must be below 2^31.
+ *
+ *   workspace  at least sv_kv_pages_workspace_bytes(num_pages, R, n) bytes
+ *              (n: forks of a kv_pages_fork call, 0 otherwise), 256-byte
+ *              aligned.  Nothing in it outlives a call; calls that may run at
+ *              the same time need their own.
+ *   status     device int32, may be NULL; ORed with
+ *                SV_DEV_BAD_BOUND    a length outside [0, max_pages_per_req*64]
+ *                SV_DEV_BAD_PAGE     an entry outside the pool, or one given
+ *                                    back that nobody held (that count stays)
+ *                SV_DEV_NO_PAGE, SV_DEV_SHARED_PAGE, SV_DEV_BAD_REQUEST
+ *              What a bit reports is left undone for that request (fork,
+ *              pair) only, as said at each call; the rest is done.
+ *
+ * kv_pages_copy: for every pair i < n and every layer, page src_ids[i] of
+ *   src_pages [layers][src_num_pages][page_bytes] is copied to page dst_ids[i]
+ *   of dst_pages [layers][dst_num_pages][page_bytes] (16-byte aligned,
+ *   page_bytes a multiple of 16, up to 2^30).  A pair with an id of -1 is
+ *   skipped; another id outside its pool sets SV_DEV_BAD_PAGE and skips the
+ *   pair.  The two pools may be one; the destinations must be distinct, and in
+ *   one pool no destination may be a source of the same call.
+ *
+ * kv_pages_fork: for every fork i < n, request children[i] becomes a
+ *   continuation of request parents[i] (of the state before the call): it gets
+ *   the parent's length and full pages, whose counts grow by one, and a page of
+ *   its own with a copy of the rows in use of the parent's last, partly filled
+ *   page (the other rows of that page keep what they hold).  So neither
+ *   writes into a page of the other when both go on.  A child must hold nothing (length 0); when a child is named
+ *   twice only the first fork counts.  A fork with an index outside [0, R), a
+ *   child in use or named before (SV_DEV_BAD_REQUEST), a parent's length out
+ *   of range or no page left for its last rows (SV_DEV_NO_PAGE) leaves the
+ *   child as it was.  A parent's entry outside the pool is passed on as it is
+ *   (SV_DEV_BAD_PAGE), counted nowhere and copied from nowhere.
+ *   Two kernels on `stream` (the second a programmatic dependent launch).
+ *
+ * kv_pages_resize: request r gets the pages of length new_lens[r] (-1: stays
+ *   as it is; 0: gives everything back).  Pages behind the new length are
+ *   given back first, over all requests (entry := -1, count - 1; a page is
+ *   free when its count reaches 0), then the longer requests get theirs.  A
+ *   request for which too few pages are left when its turn comes keeps its
+ *   length (SV_DEV_NO_PAGE), and so do the later ones that need pages.  A
+ *   request that would grow inside a partly filled page that others hold too
+ *   keeps its length (SV_DEV_SHARED_PAGE): fork it first, the child can grow.
+ *   A request with a length out of range, old or new, stays as it is.
+ *   One kernel on `stream`.
+ *
+ * kv_pages_compact: with n pages in use (count not 0), those at ids >= n move
+ *   into the free ids below n, in ascending order on both sides, in every
+ *   layer; the counts and the table entries in use follow.  page_map [num_pages]
+ *   receives every page's new id (-1: it was free), num_live [1] receives n.
+ *   An entry in use that names a free page becomes -1, one outside the pool
+ *   stays (SV_DEV_BAD_PAGE both).  Pages from n on keep what they hold.
+ *   kv_lens is only read.  Two kernels on `stream`, as above.
+ * ---------------------------------------------------------------------- */
+size_t sv_kv_pages_workspace_bytes(int num_pages, int R, int n);
+
+sv_status kv_pages_copy(const void* src_pages, int src_num_pages, void* dst_pages, int dst_num_pages,
+                        int layers, size_t page_bytes, const int32_t* src_ids,
+                        const int32_t* dst_ids, int n, int32_t* status, sv_stream_t stream);
+
+sv_status kv_pages_fork(void* kv_pages, int num_pages, int page_size, int layers, size_t row_bytes,
+                        const int32_t* ref_counts_in, const int32_t* block_table_in,
+                        const int32_t* kv_lens_in, int R, int max_pages_per_req,
+                        const int32_t* parents, const int32_t* children, int n,
+                        int32_t* ref_counts_out, int32_t* block_table_out, int32_t* kv_lens_out,
+                        void* workspace, size_t workspace_bytes, int32_t* status,
+                        sv_stream_t stream);
+
+sv_status kv_pages_resize(const int32_t* ref_counts_in, int num_pages, int page_size,
+                          const int32_t* block_table_in, const int32_t* kv_lens_in, int R,
+                          int max_pages_per_req, const int32_t* new_lens, int32_t* ref_counts_out,
+                          int32_t* block_table_out, int32_t* kv_lens_out, void* workspace,
+                          size_t workspace_bytes, int32_t* status, sv_stream_t stream);
+
+sv_status kv_pages_compact(void* kv_pages, int num_pages, int page_size, int layers,
+                           size_t row_bytes, const int32_t* ref_counts_in,
+                           const int32_t* block_table_in, const int32_t* kv_lens, int R,
+                           int max_pages_per_req, int32_t* ref_counts_out,
+                           int32_t* block_table_out, int32_t* page_map, int32_t* num_live,
+                           void* workspace, size_t workspace_bytes, int32_t* status,
+                           sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * mla_lse_combine

@@ -1,0 +1,141 @@
+"""Sequential CPU oracle for the page bookkeeping of the paged latent cache.
+
+TEST INFRASTRUCTURE, NOT PRODUCT CODE.  It shares no code with the CUDA
+library and imports nothing from it.  One request, fork or page after the
+other, on copies of the inputs; every function returns the new state and the
+device status bits.  Pools are [layers, pages, 64, bytes] arrays.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+PAGE = 64
+BAD_PAGE, BAD_BOUND, SHARED_PAGE, NO_PAGE, BAD_REQUEST = 0x1, 0x2, 0x10, 0x20, 0x40
+
+
+def pages_of(n: int) -> int:
+    return -(-int(n) // PAGE)
+
+
+def ref_pages_copy(src, dst, src_ids, dst_ids):
+    out, status = dst.copy(), 0
+    for a, b in zip(src_ids, dst_ids):
+        if a == -1 or b == -1:
+            continue
+        if not (0 <= a < src.shape[1] and 0 <= b < dst.shape[1]):
+            status |= BAD_PAGE
+            continue
+        out[:, b] = src[:, a]
+    return out, status
+
+
+def ref_pages_resize(ref_counts, block_table, kv_lens, new_lens):
+    refs, table, lens = ref_counts.copy(), block_table.copy(), kv_lens.copy()
+    P, (R, mp) = len(refs), table.shape
+    cap, status = mp * PAGE, 0
+    todo = []
+    for r in range(R):
+        old, new = int(kv_lens[r]), int(new_lens[r])
+        if not (0 <= old <= cap and -1 <= new <= cap):
+            status |= BAD_BOUND
+            continue
+        if new == -1:
+            continue
+        todo.append((r, old, new))
+        for j in range(pages_of(new), pages_of(old)):
+            p = int(table[r, j])
+            if not 0 <= p < P or refs[p] <= 0:
+                status |= BAD_PAGE
+            else:
+                refs[p] -= 1
+            table[r, j] = -1
+    free = [int(p) for p in np.flatnonzero(refs == 0)]
+    before = refs.copy()
+    asked = 0
+    for r, old, new in todo:
+        if new > old and old % PAGE:
+            p = int(table[r, old // PAGE])
+            if not 0 <= p < P:
+                status |= BAD_PAGE
+                continue
+            if before[p] > 1:
+                status |= SHARED_PAGE
+                continue
+        need = max(0, pages_of(new) - pages_of(old))
+        first, asked = asked, asked + need
+        if need and asked > len(free):
+            status |= NO_PAGE
+            continue
+        for i in range(need):
+            table[r, pages_of(old) + i] = free[first + i]
+            refs[free[first + i]] = 1
+        lens[r] = new
+    return refs, table, lens, status
+
+
+def ref_pages_fork(pool, ref_counts, block_table, kv_lens, parents, children):
+    pool, refs, table, lens = pool.copy(), ref_counts.copy(), block_table.copy(), kv_lens.copy()
+    P, (R, mp) = len(refs), table.shape
+    free = [int(p) for p in np.flatnonzero(refs == 0)]
+    status, asked, named = 0, 0, set()
+    for a, b in zip(map(int, parents), map(int, children)):
+        first = b not in named
+        named.add(b)
+        if not (0 <= a < R and 0 <= b < R) or kv_lens[b] != 0 or not first:
+            status |= BAD_REQUEST
+            continue
+        n = int(kv_lens[a])
+        if not 0 <= n <= mp * PAGE:
+            status |= BAD_BOUND
+            continue
+        full, tail = divmod(n, PAGE)
+        if tail:
+            asked += 1
+            if asked > len(free):
+                status |= NO_PAGE
+                continue
+        for j in range(full):
+            p = int(block_table[a, j])
+            table[b, j] = p
+            if 0 <= p < P:
+                refs[p] += 1
+            else:
+                status |= BAD_PAGE
+        if tail:
+            p, q = int(block_table[a, full]), free[asked - 1]
+            table[b, full] = q
+            refs[q] = 1
+            if 0 <= p < P:
+                pool[:, q, :tail] = pool[:, p, :tail]
+            else:
+                status |= BAD_PAGE
+        lens[b] = n
+    return pool, refs, table, lens, status
+
+
+def ref_pages_compact(pool, ref_counts, block_table, kv_lens):
+    pool, table = pool.copy(), block_table.copy()
+    P, (R, mp) = len(ref_counts), table.shape
+    live = [int(p) for p in np.flatnonzero(ref_counts)]
+    n, status = len(live), 0
+    to = {p: p for p in live if p < n}
+    for p, q in zip([p for p in live if p >= n], [q for q in range(n) if q not in to]):
+        to[p] = q
+        pool[:, q] = pool[:, p]
+    refs, page_map = np.zeros_like(ref_counts), np.full(P, -1, np.int32)
+    for p, q in to.items():
+        refs[q], page_map[p] = ref_counts[p], q
+    for r in range(R):
+        held = int(kv_lens[r])
+        if not 0 <= held <= mp * PAGE:
+            status |= BAD_BOUND
+            held = max(0, min(held, mp * PAGE))
+        for j in range(pages_of(held)):
+            p = int(table[r, j])
+            if not 0 <= p < P:
+                status |= BAD_PAGE
+            else:
+                table[r, j] = page_map[p]
+                if page_map[p] < 0:
+                    status |= BAD_PAGE
+    return pool, refs, table, page_map, n, status

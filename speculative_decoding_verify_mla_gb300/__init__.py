@@ -7,6 +7,9 @@ from .binding import (  # noqa: F401
     EXPORTED_SYMBOLS,
     SV_DEV_BAD_BOUND,
     SV_DEV_BAD_PAGE,
+    SV_DEV_BAD_REQUEST,
+    SV_DEV_NO_PAGE,
+    SV_DEV_SHARED_PAGE,
     SV_DEV_TIMEOUT,
     FORM_AUTO,
     FORM_STACKED,
@@ -17,6 +20,11 @@ from .binding import (  # noqa: F401
     attention_workspace_bytes,
     greedy_workspace,
     greedy_workspace_bytes,
+    kv_pages_compact,
+    kv_pages_copy,
+    kv_pages_fork,
+    kv_pages_resize,
+    kv_pages_workspace_bytes,
     load_library,
     mla_kv_append,
     mla_lse_combine,

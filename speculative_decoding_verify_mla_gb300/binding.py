@@ -8,6 +8,7 @@ is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -31,6 +32,9 @@ FORM_AUTO, FORM_TWO_CTA, FORM_STACKED = 0, 1, 2
 SV_DEV_BAD_PAGE = 0x1
 SV_DEV_BAD_BOUND = 0x2
 SV_DEV_TIMEOUT = 0x4
+SV_DEV_SHARED_PAGE = 0x10
+SV_DEV_NO_PAGE = 0x20
+SV_DEV_BAD_REQUEST = 0x40
 
 EXPORTED_SYMBOLS = (
     "sv_status_string",
@@ -46,6 +50,11 @@ EXPORTED_SYMBOLS = (
     "mla_verify_decode_gated",
     "mla_wuv_project",
     "mla_verify_decode_kv8",
+    "sv_kv_pages_workspace_bytes",
+    "kv_pages_copy",
+    "kv_pages_fork",
+    "kv_pages_resize",
+    "kv_pages_compact",
 )
 
 _lib = None
@@ -114,6 +123,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             _c_void_p, _c_void_p, _c_int, _c_int, _c_float, _c_int, _c_int, _c_void_p, _c_size,
             _c_void_p, _c_void_p, _c_void_p, _c_void_p]
         lib.mla_verify_decode_kv8.restype = _c_int
+        p, i, z = _c_void_p, _c_int, _c_size
+        lib.sv_kv_pages_workspace_bytes.argtypes = [i, i, i]
+        lib.sv_kv_pages_workspace_bytes.restype = z
+        lib.kv_pages_copy.argtypes = [p, i, p, i, i, z, p, p, i, p, p]
+        lib.kv_pages_copy.restype = i
+        lib.kv_pages_fork.argtypes = [p, i, i, i, z, p, p, p, i, i, p, p, i, p, p, p, p, z, p, p]
+        lib.kv_pages_fork.restype = i
+        lib.kv_pages_resize.argtypes = [p, i, i, p, p, i, i, p, p, p, p, p, z, p, p]
+        lib.kv_pages_resize.restype = i
+        lib.kv_pages_compact.argtypes = [p, i, i, i, z, p, p, p, i, i, p, p, p, p, p, z, p, p]
+        lib.kv_pages_compact.restype = i
         _lib = lib
         return lib
 
@@ -378,3 +398,160 @@ def mla_wuv_project(x: torch.Tensor, w_uv: torch.Tensor, out_v: torch.Tensor | N
     code = lib.mla_wuv_project(_ptr(x), _ptr(w_uv), T, H, v_dim, _ptr(out_v), _ptr(status), _stream(dev))
     _check_status("mla_wuv_project", code)
     return out_v
+
+
+# ------------------------------------------------------------------ pages of the cache
+def _on_device(dev: torch.device):
+    """The launch goes to the current device: make it the tensors' own."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def kv_pages_workspace_bytes(num_pages: int, R: int, n: int = 0) -> int:
+    """Workspace of a kv_pages_* call over a pool of num_pages pages and R
+    requests (n: forks of a kv_pages_fork call)."""
+    return int(load_library().sv_kv_pages_workspace_bytes(num_pages, R, n))
+
+
+def _pool_shape(name: str, t: torch.Tensor):
+    """(layers, pages, bytes of a row) of [P, 64, W] or [layers, P, 64, W]."""
+    _check(t.device.type == "cuda", "tensors must live on a CUDA device")
+    _check(t.dim() in (3, 4) and t.shape[-2] == SV_PAGE_SIZE and t.is_contiguous(),
+           f"{name} must be contiguous, [P, 64, W] or [layers, P, 64, W]")
+    return (t.shape[0] if t.dim() == 4 else 1), t.shape[-3], t.shape[-1] * t.element_size()
+
+
+def _ints(dev: torch.device, **tensors):
+    for name, t in tensors.items():
+        _check(t.dtype == torch.int32 and t.device == dev and t.is_contiguous(), f"{name}: int32, contiguous, on {dev}")
+
+
+def _like(name: str, out: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty_like(like)
+    _check(out.dtype == like.dtype and out.device == like.device and out.shape == like.shape and out.is_contiguous(),
+           f"{name}: {like.dtype}, contiguous, {tuple(like.shape)} on {like.device}")
+    return out
+
+
+def _status_ok(status: torch.Tensor | None, dev: torch.device):
+    if status is not None:
+        _check(status.dtype == torch.int32 and status.device == dev and status.numel() >= 1, f"status: int32 on {dev}")
+
+
+def _pages_workspace(dev: torch.device, workspace: torch.Tensor | None, need: int) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
+    return workspace
+
+
+def _tables(ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor):
+    dev = ref_counts.device
+    _check(dev.type == "cuda", "tensors must live on a CUDA device")
+    _ints(dev, ref_counts=ref_counts, block_table=block_table, kv_lens=kv_lens)
+    _check(ref_counts.dim() == 1, "ref_counts must be [P]")
+    _check(block_table.dim() == 2, "block_table must be [R, max_pages]")
+    _check(kv_lens.shape == block_table.shape[:1], "kv_lens must be [R]")
+    return dev, ref_counts.shape[0], block_table.shape[0], block_table.shape[1]
+
+
+def kv_pages_copy(src_pages: torch.Tensor, dst_pages: torch.Tensor, src_ids: torch.Tensor, dst_ids: torch.Tensor,
+                  status: torch.Tensor | None = None) -> torch.Tensor:
+    """Copy pages src_ids [n] of src_pages to pages dst_ids [n] of dst_pages
+    (in place), in every layer.  The pools are [P, 64, W] or [layers, P, 64, W]
+    and may be one tensor; an id of -1 skips the pair.  Destinations must be
+    distinct and, in one pool, no source of the call."""
+    lib = load_library()
+    layers, src_p, row = _pool_shape("src_pages", src_pages)
+    dst_layers, dst_p, dst_row = _pool_shape("dst_pages", dst_pages)
+    dev = dst_pages.device
+    _check(src_pages.device == dev, f"src_pages must be on {dev}")
+    _check(src_pages.dtype == dst_pages.dtype and layers == dst_layers and row == dst_row,
+           "the pools must have the same type, layers and row width")
+    _ints(dev, src_ids=src_ids, dst_ids=dst_ids)
+    _check(src_ids.dim() == 1 and src_ids.shape == dst_ids.shape, "src_ids and dst_ids must be [n]")
+    _status_ok(status, dev)
+    with _on_device(dev):
+        code = lib.kv_pages_copy(_ptr(src_pages), src_p, _ptr(dst_pages), dst_p, layers, row * SV_PAGE_SIZE,
+                                 _ptr(src_ids), _ptr(dst_ids), src_ids.shape[0], _ptr(status), _stream(dev))
+    _check_status("kv_pages_copy", code)
+    return dst_pages
+
+
+def kv_pages_fork(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                  parents: torch.Tensor, children: torch.Tensor, ref_counts_out: torch.Tensor | None = None,
+                  block_table_out: torch.Tensor | None = None, kv_lens_out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    """Make request children[i] a continuation of parents[i]: it shares the
+    parent's full pages and gets a copy of its last, partly filled one in
+    kv_pages (in place).  Returns (ref_counts, block_table, kv_lens) after the
+    forks, in new tensors or in the *_out tensors, which may be the inputs."""
+    lib = load_library()
+    dev, P, R, max_pages = _tables(ref_counts, block_table, kv_lens)
+    layers, pages, row = _pool_shape("kv_pages", kv_pages)
+    _check(pages == P and kv_pages.device == dev, f"kv_pages must have ref_counts' {P} pages, on {dev}")
+    _ints(dev, parents=parents, children=children)
+    _check(parents.dim() == 1 and parents.shape == children.shape, "parents and children must be [n]")
+    _status_ok(status, dev)
+    n = parents.shape[0]
+    outs = (_like("ref_counts_out", ref_counts_out, ref_counts), _like("block_table_out", block_table_out, block_table),
+            _like("kv_lens_out", kv_lens_out, kv_lens))
+    ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R, n))
+    with _on_device(dev):
+        code = lib.kv_pages_fork(_ptr(kv_pages), P, SV_PAGE_SIZE, layers, row, _ptr(ref_counts), _ptr(block_table),
+                                 _ptr(kv_lens), R, max_pages, _ptr(parents), _ptr(children), n, *map(_ptr, outs),
+                                 _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(dev))
+    _check_status("kv_pages_fork", code)
+    return outs
+
+
+def kv_pages_resize(ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, new_lens: torch.Tensor,
+                    ref_counts_out: torch.Tensor | None = None, block_table_out: torch.Tensor | None = None,
+                    kv_lens_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None):
+    """Give request r the pages of length new_lens[r] (-1: as it is, 0: none),
+    handing out the lowest free pages and taking back those behind the new
+    length.  Returns (ref_counts, block_table, kv_lens) as kv_pages_fork."""
+    lib = load_library()
+    dev, P, R, max_pages = _tables(ref_counts, block_table, kv_lens)
+    _ints(dev, new_lens=new_lens)
+    _check(new_lens.shape == kv_lens.shape, "new_lens must be [R]")
+    _status_ok(status, dev)
+    outs = (_like("ref_counts_out", ref_counts_out, ref_counts), _like("block_table_out", block_table_out, block_table),
+            _like("kv_lens_out", kv_lens_out, kv_lens))
+    ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R))
+    with _on_device(dev):
+        code = lib.kv_pages_resize(_ptr(ref_counts), P, SV_PAGE_SIZE, _ptr(block_table), _ptr(kv_lens), R, max_pages,
+                                   _ptr(new_lens), *map(_ptr, outs), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _ptr(status), _stream(dev))
+    _check_status("kv_pages_resize", code)
+    return outs
+
+
+def kv_pages_compact(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                     ref_counts_out: torch.Tensor | None = None, block_table_out: torch.Tensor | None = None,
+                     page_map: torch.Tensor | None = None, num_live: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    """Move the pages in use to the front of kv_pages (in place).  Returns
+    (ref_counts, block_table, page_map [P]: every page's new id or -1,
+    num_live [1]); the *_out tensors may be the inputs."""
+    lib = load_library()
+    dev, P, R, max_pages = _tables(ref_counts, block_table, kv_lens)
+    layers, pages, row = _pool_shape("kv_pages", kv_pages)
+    _check(pages == P and kv_pages.device == dev, f"kv_pages must have ref_counts' {P} pages, on {dev}")
+    _status_ok(status, dev)
+    outs = (_like("ref_counts_out", ref_counts_out, ref_counts), _like("block_table_out", block_table_out, block_table),
+            _like("page_map", page_map, ref_counts))
+    if num_live is None:
+        num_live = torch.empty(1, dtype=torch.int32, device=dev)
+    _ints(dev, num_live=num_live)
+    _check(num_live.numel() == 1, "num_live must be [1]")
+    ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R))
+    with _on_device(dev):
+        code = lib.kv_pages_compact(_ptr(kv_pages), P, SV_PAGE_SIZE, layers, row, _ptr(ref_counts), _ptr(block_table),
+                                    _ptr(kv_lens), R, max_pages, *map(_ptr, outs), _ptr(num_live), _ptr(ws),
+                                    ws.numel() * ws.element_size(), _ptr(status), _stream(dev))
+    _check_status("kv_pages_compact", code)
+    return (*outs, num_live)

@@ -1,0 +1,806 @@
+// kv_pages.cu - the pages of the paged latent cache: copying pages, forking a
+// request, giving requests the pages of a new length, closing the holes of a
+// fragmented pool.
+//
+// State.  ref_counts[p] counts the table entries that hold page p; a page is
+// free exactly when its count is 0, so the counts are the whole allocator (no
+// free list to keep in step).  Request r holds the first ceil(kv_lens[r]/64)
+// entries of its table row.  New pages are always the lowest free ones, given
+// out in request (fork) order, so that results never depend on timing: counts
+// change by integer atomics, whose order does not matter, and every other
+// word has one writer.
+//
+// The bookkeeping of one call is a single kernel of one thread-block cluster
+// (one CTA for small pools, eight for larger ones): its phases - take back,
+// rank the requests' needs, rank the free pages, hand out - depend on each
+// other, and a cluster barrier between them costs far less than a launch.
+// Ranking is a prefix sum over warp ballots; the CTAs' totals meet in
+// distributed shared memory.  What bounds it is latency (a few dependent
+// round trips to L2), not bytes.  The pages themselves move in a second
+// kernel over the whole GPU, a programmatic dependent launch, bound by HBM:
+// two bytes of traffic per byte moved.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sv_cluster.cuh"
+#include "sv_ptx.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kMetaThreads = 1024;
+constexpr int kMetaWarps = kMetaThreads / 32;
+constexpr int kItems = 8;                            // pages per thread and tile
+constexpr int kTile = kMetaThreads * kItems;         // pages per CTA and tile
+constexpr int kClusterMax = 8;
+// Pools and tables of at most this many words together take one CTA.
+constexpr long long kOneCtaWords = 16384;
+constexpr int kCopyThreads = 256;
+constexpr int kChunkBytes = kCopyThreads * 16 * 4;   // one CTA pass: four 16-byte words per thread
+
+struct MetaShared {
+  int seg[kItems * kMetaWarps];
+  int wsum[kMetaWarps];
+  int total;
+  int totals[2][kClusterMax];
+};
+
+// The position of this CTA in its cluster and the parity of its next exchange.
+struct Group {
+  uint32_t rank, size;
+  int parity;
+};
+
+__device__ __forceinline__ void group_sync(const Group& g) {
+  if (g.size == 1)
+    __syncthreads();
+  else
+    cluster_sync();
+}
+
+// Sum of one number per CTA over the ranks below this one (*before) and over
+// the cluster (*all); `mine` is the same in every thread of the CTA.  Slots
+// alternate, so a CTA may be one exchange ahead of a reader.
+__device__ __forceinline__ void group_sum(Group& g, MetaShared& s, int mine, int* before, int* all) {
+  if (g.size == 1) {
+    *before = 0;
+    *all = mine;
+    return;
+  }
+  if (threadIdx.x < g.size)
+    cluster_st(cluster_map(&s.totals[g.parity][g.rank], threadIdx.x), (uint32_t)mine);
+  cluster_sync();
+  int b = 0, a = 0;
+  for (uint32_t r = 0; r < g.size; ++r) {
+    const int v = s.totals[g.parity][r];
+    if (r < g.rank) b += v;
+    a += v;
+  }
+  *before = b;
+  *all = a;
+  g.parity ^= 1;
+}
+
+// Exclusive prefix sum over the CTA in thread order.
+__device__ __forceinline__ int block_scan_excl(MetaShared& s, int v, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s.wsum[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s.wsum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+      if (lane >= o) w += y;
+    }
+    s.wsum[lane] = w;
+  }
+  __syncthreads();
+  const int before = warp > 0 ? s.wsum[warp - 1] : 0;
+  *total = s.wsum[kMetaWarps - 1];
+  __syncthreads();
+  return before + incl - v;
+}
+
+// Ranks the flagged pages of one cluster-wide tile: item k of thread t of CTA
+// c is page base + c * kTile + k * 1024 + t, so the loads are coalesced and
+// page order is (CTA, item, warp, lane).  rank[k] is the number of flagged
+// pages before item k's in the tile; returns the tile's flagged pages.
+__device__ __forceinline__ int tile_rank(Group& g, MetaShared& s, const bool (&flag)[kItems], int (&rank)[kItems]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned ballot[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    ballot[k] = __ballot_sync(0xFFFFFFFFu, flag[k]);
+    if (lane == k) s.seg[k * kMetaWarps + warp] = __popc(ballot[k]);
+  }
+  __syncthreads();
+  int v = 0, incl = 0;
+  if (threadIdx.x < kItems * kMetaWarps) {
+    v = incl = s.seg[threadIdx.x];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s.wsum[warp] = incl;
+  }
+  __syncthreads();
+  int total = 0, mine = 0;
+#pragma unroll
+  for (int w = 0; w < kItems; ++w) {
+    if (w < warp) mine += s.wsum[w];
+    total += s.wsum[w];
+  }
+  if (threadIdx.x < kItems * kMetaWarps) s.seg[threadIdx.x] = mine + incl - v;
+  int before, all;
+  group_sum(g, s, total, &before, &all);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kItems; ++k)
+    rank[k] = before + s.seg[k * kMetaWarps + warp] + __popc(ballot[k] & ((1u << lane) - 1u));
+  __syncthreads();
+  return all;
+}
+
+// The first `want` free pages in ascending order into list[0..); returns how
+// many there are, at most the count at which the search stopped (>= want).
+__device__ int list_free(Group& g, MetaShared& s, const int32_t* ref_counts, int P, int want, int* list) {
+  int found = 0;
+  const long long step = (long long)kTile * g.size;
+  for (long long base = 0; base < P && found < want; base += step) {
+    bool flag[kItems];
+    int rank[kItems];
+    const long long p0 = base + (long long)g.rank * kTile + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const long long p = p0 + k * kMetaThreads;
+      flag[k] = p < P && __ldcg(ref_counts + p) == 0;
+    }
+    const int all = tile_rank(g, s, flag, rank);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k)
+      if (flag[k] && found + rank[k] < want) list[found + rank[k]] = (int)(p0 + k * kMetaThreads);
+    found += all;
+  }
+  return found;
+}
+
+__device__ __forceinline__ void report(int32_t* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ Group make_group() { return Group{cluster_rank(), cluster_size(), 0}; }
+
+// ---------------------------------------------------------------------------
+// resize
+// ---------------------------------------------------------------------------
+struct ResizeArgs {
+  const int32_t *ref_in, *table_in, *lens_in, *new_lens;
+  int32_t *ref_out, *table_out, *lens_out, *status;
+  int *prefix, *list;  // workspace: pages asked for before request r; free pages
+  int P, R, mp;
+};
+
+struct Change {
+  bool apply;      // the request changes
+  int have, want;  // entries held before and after
+  int old_len, new_len;
+};
+__device__ __forceinline__ Change read_change(const ResizeArgs& a, int r, bool tell) {
+  Change c;
+  const int cap = a.mp * SV_PAGE_SIZE;
+  c.old_len = a.lens_in[r];
+  c.new_len = __ldg(a.new_lens + r);
+  const bool bad = c.old_len < 0 || c.old_len > cap || c.new_len < -1 || c.new_len > cap;
+  if (bad && tell) report(a.status, SV_DEV_BAD_BOUND);
+  c.apply = !bad && c.new_len >= 0;
+  c.have = c.apply ? (c.old_len + SV_PAGE_SIZE - 1) / SV_PAGE_SIZE : 0;
+  c.want = c.apply ? (c.new_len + SV_PAGE_SIZE - 1) / SV_PAGE_SIZE : 0;
+  return c;
+}
+// A longer request writes behind its last row: refused where that row's page
+// is held by others too, or is no page (counts after everything was taken
+// back; handing out pages does not change the count of a page in use).
+__device__ __forceinline__ bool may_grow(const ResizeArgs& a, int r, const Change& c, bool tell) {
+  if (!c.apply || c.new_len <= c.old_len || c.old_len % SV_PAGE_SIZE == 0) return c.apply;
+  const int p = __ldcg(a.table_out + (long long)r * a.mp + c.old_len / SV_PAGE_SIZE);
+  if (p < 0 || p >= a.P) {
+    if (tell) report(a.status, SV_DEV_BAD_PAGE);
+    return false;
+  }
+  if (__ldcg(a.ref_out + p) <= 1) return true;
+  if (tell) report(a.status, SV_DEV_SHARED_PAGE);
+  return false;
+}
+
+__global__ void __launch_bounds__(kMetaThreads) resize_kernel(const ResizeArgs a) {
+  __shared__ MetaShared s;
+  Group g = make_group();
+  const int lane = threadIdx.x & 31;
+  const int threads = (int)g.size * kMetaThreads, tid = (int)g.rank * kMetaThreads + threadIdx.x;
+  if (a.ref_out != a.ref_in) {
+    for (long long p = tid; p < a.P; p += threads) a.ref_out[p] = __ldg(a.ref_in + p);
+    group_sync(g);
+  }
+  // take back: a warp per request
+  for (int r = tid >> 5; r < a.R; r += threads >> 5) {
+    const Change c = read_change(a, r, lane == 0);
+    const long long row = (long long)r * a.mp;
+    for (int j = lane; j < a.mp; j += 32) {
+      int p = a.table_in[row + j];
+      const bool drop = j >= c.want && j < c.have;
+      if (drop) {
+        if (p < 0 || p >= a.P) {
+          report(a.status, SV_DEV_BAD_PAGE);
+        } else if (atomicSub(a.ref_out + p, 1) <= 0) {
+          atomicAdd(a.ref_out + p, 1);  // held by nobody: stays as it was
+          report(a.status, SV_DEV_BAD_PAGE);
+        }
+        p = -1;
+      }
+      if (drop || a.table_out != a.table_in) a.table_out[row + j] = p;
+    }
+  }
+  group_sync(g);
+  // rank the needs in request order (every CTA the same sums, rank 0 writes)
+  int asked = 0;
+  for (int r0 = 0; r0 < a.R; r0 += kMetaThreads) {
+    const int r = r0 + (int)threadIdx.x;
+    int need = 0;
+    if (r < a.R) {
+      const Change c = read_change(a, r, false);
+      if (c.want > c.have && may_grow(a, r, c, false)) need = c.want - c.have;
+    }
+    int total;
+    const int before = block_scan_excl(s, need, &total);
+    if (r < a.R && g.rank == 0) a.prefix[r] = asked + before;
+    asked += total;
+  }
+  const int found = list_free(g, s, a.ref_out, a.P, asked, a.list);
+  group_sync(g);
+  // hand out: a warp per request
+  for (int r = tid >> 5; r < a.R; r += threads >> 5) {
+    const Change c = read_change(a, r, false);
+    bool done = may_grow(a, r, c, lane == 0);
+    if (done && c.want > c.have) {
+      const int first = __ldcg(a.prefix + r);
+      if (first + (c.want - c.have) > found) {
+        done = false;
+        if (lane == 0) report(a.status, SV_DEV_NO_PAGE);
+      } else {
+        for (int j = c.have + lane; j < c.want; j += 32) {
+          const int p = __ldcg(a.list + first + j - c.have);
+          a.table_out[(long long)r * a.mp + j] = p;
+          a.ref_out[p] = 1;
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) a.lens_out[r] = done ? c.new_len : c.old_len;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fork
+// ---------------------------------------------------------------------------
+struct ForkArgs {
+  const int32_t *ref_in, *table_in, *lens_in, *parents, *children;
+  int32_t *ref_out, *table_out, *lens_out, *status;
+  int *claim, *prefix, *list;  // workspace: the first fork onto a child; tails before fork i; free pages
+  int4* moves;                 // workspace: tail page, its copy, rows (0: nothing to copy), length (-1: not done)
+  int P, R, mp, n;
+};
+
+struct Fork {
+  bool valid;
+  int parent, child, len;
+};
+__device__ __forceinline__ Fork read_fork(const ForkArgs& a, int i, bool tell) {
+  Fork f;
+  f.parent = __ldg(a.parents + i);
+  f.child = __ldg(a.children + i);
+  f.valid = f.parent >= 0 && f.parent < a.R && f.child >= 0 && f.child < a.R;
+  f.len = 0;
+  if (f.valid) {
+    f.len = a.lens_in[f.parent];
+    // the child holds nothing yet, and this is the first fork onto it
+    f.valid = a.lens_in[f.child] == 0 && __ldcg(a.claim + f.child) == i;
+  }
+  if (!f.valid && tell) report(a.status, SV_DEV_BAD_REQUEST);
+  if (f.valid && (f.len < 0 || f.len > a.mp * SV_PAGE_SIZE)) {
+    f.valid = false;
+    if (tell) report(a.status, SV_DEV_BAD_BOUND);
+  }
+  return f;
+}
+
+__global__ void __launch_bounds__(kMetaThreads) fork_kernel(const ForkArgs a) {
+  __shared__ MetaShared s;
+  Group g = make_group();
+  const int lane = threadIdx.x & 31;
+  const int threads = (int)g.size * kMetaThreads, tid = (int)g.rank * kMetaThreads + threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.ref_out != a.ref_in)
+    for (long long p = tid; p < a.P; p += threads) a.ref_out[p] = __ldg(a.ref_in + p);
+  if (a.table_out != a.table_in)
+    for (long long e = tid; e < (long long)a.R * a.mp; e += threads) a.table_out[e] = __ldg(a.table_in + e);
+  for (int i = tid; i < a.n; i += threads) {
+    const int c = __ldg(a.children + i);
+    if (c >= 0 && c < a.R) a.claim[c] = 0x7FFFFFFF;
+  }
+  group_sync(g);
+  for (int i = tid; i < a.n; i += threads) {
+    const int c = __ldg(a.children + i);
+    if (c >= 0 && c < a.R) atomicMin(a.claim + c, i);
+  }
+  group_sync(g);
+  int asked = 0;
+  for (int i0 = 0; i0 < a.n; i0 += kMetaThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    int need = 0;
+    if (i < a.n) {
+      const Fork f = read_fork(a, i, false);
+      need = f.valid && f.len % SV_PAGE_SIZE != 0;
+    }
+    int total;
+    const int before = block_scan_excl(s, need, &total);
+    if (i < a.n && g.rank == 0) a.prefix[i] = asked + before;
+    asked += total;
+  }
+  // the free pages as they were before the call: counts only grow below
+  const int found = list_free(g, s, a.ref_out, a.P, asked, a.list);
+  if (a.lens_out != a.lens_in)
+    for (int r = tid; r < a.R; r += threads) a.lens_out[r] = a.lens_in[r];
+  group_sync(g);
+  for (int i = tid >> 5; i < a.n; i += threads >> 5) {
+    const Fork f = read_fork(a, i, lane == 0);
+    const int full = f.len / SV_PAGE_SIZE, tail = f.len % SV_PAGE_SIZE;
+    bool done = f.valid;
+    int fresh = -1;
+    if (done && tail != 0) {
+      const int at = __ldcg(a.prefix + i);
+      done = at < found;
+      if (done)
+        fresh = __ldcg(a.list + at);
+      else if (lane == 0)
+        report(a.status, SV_DEV_NO_PAGE);
+    }
+    int4 move = make_int4(-1, -1, 0, done ? f.len : -1);
+    if (done) {
+      const int32_t* from = a.table_in + (long long)f.parent * a.mp;
+      int32_t* to = a.table_out + (long long)f.child * a.mp;
+      for (int j = lane; j < full; j += 32) {
+        const int p = from[j];
+        to[j] = p;
+        if (p >= 0 && p < a.P)
+          atomicAdd(a.ref_out + p, 1);
+        else
+          report(a.status, SV_DEV_BAD_PAGE);
+      }
+      if (lane == 0 && tail != 0) {
+        const int p = from[full];
+        to[full] = fresh;
+        a.ref_out[fresh] = 1;
+        if (p >= 0 && p < a.P)
+          move = make_int4(p, fresh, tail, f.len);
+        else
+          report(a.status, SV_DEV_BAD_PAGE);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) a.moves[i] = move;
+  }
+  // the children's lengths last: until here every warp looks at the lengths
+  // as they were before the call, also when they are updated in place
+  group_sync(g);
+  for (int i = tid; i < a.n; i += threads) {
+    const int len = __ldcg(&a.moves[i].w);
+    if (len >= 0) a.lens_out[__ldg(a.children + i)] = len;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// compact
+// ---------------------------------------------------------------------------
+struct CompactArgs {
+  const int32_t* ref_in;
+  int32_t *ref_out, *page_map, *num_live;
+  int2* live;   // workspace: (page, count) of the live pages at or above the live count, by live rank
+  int* holes;   // workspace: the free pages below it, ascending
+  int* header;  // workspace: live pages below the live count; moves
+  int2* moves;  // workspace
+  int P;
+};
+
+__global__ void __launch_bounds__(kMetaThreads) compact_kernel(const CompactArgs a) {
+  __shared__ MetaShared s;
+  Group g = make_group();
+  const int threads = (int)g.size * kMetaThreads, tid = (int)g.rank * kMetaThreads + threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int mine = 0;
+  for (long long p = tid; p < a.P; p += threads) mine += a.ref_in[p] != 0;
+  int total, before, n;
+  block_scan_excl(s, mine, &total);
+  group_sync(g);  // every CTA runs (its shared memory may be written from now on)
+  group_sum(g, s, total, &before, &n);
+  // rank the live pages; what does not move is settled here
+  int rank0 = 0;
+  const long long step = (long long)kTile * g.size;
+  for (long long base = 0; base < a.P; base += step) {
+    bool flag[kItems];
+    int rank[kItems], ref[kItems];
+    const long long p0 = base + (long long)g.rank * kTile + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const long long p = p0 + k * kMetaThreads;
+      ref[k] = p < a.P ? a.ref_in[p] : 0;
+      flag[k] = ref[k] != 0;
+    }
+    const int all = tile_rank(g, s, flag, rank);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const long long q = p0 + k * kMetaThreads;
+      if (q >= a.P) continue;
+      const int p = (int)q, below = rank0 + rank[k];
+      if (p == n) a.header[0] = below;
+      if (p < n) {
+        if (flag[k])
+          a.ref_out[p] = ref[k];
+        else
+          a.holes[p - below] = p;
+      } else {
+        if (flag[k]) a.live[below] = make_int2(p, ref[k]);
+        a.ref_out[p] = 0;
+      }
+      a.page_map[p] = flag[k] && p < n ? p : -1;
+    }
+    rank0 += all;
+  }
+  group_sync(g);
+  // the j-th live page above the count goes into the j-th hole below it
+  const int kept = n < a.P ? __ldcg(a.header) : n;
+  for (int j = tid; j < n - kept; j += threads) {
+    const int2 l = __ldcg(a.live + kept + j);
+    const int h = __ldcg(a.holes + j);
+    a.page_map[l.x] = h;
+    a.ref_out[h] = l.y;
+    a.moves[j] = make_int2(l.x, h);
+  }
+  if (tid == 0) {
+    a.header[1] = n - kept;
+    *a.num_live = n;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// moving pages
+// ---------------------------------------------------------------------------
+// One chunk of at most kChunkBytes (a multiple of 16).
+__device__ __forceinline__ void copy_chunk(const uint8_t* src, uint8_t* dst, int bytes) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const int words = bytes >> 4;
+  uint4 v[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if ((int)threadIdx.x + u * kCopyThreads < words) v[u] = __ldcs(s + threadIdx.x + u * kCopyThreads);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if ((int)threadIdx.x + u * kCopyThreads < words) __stcs(d + threadIdx.x + u * kCopyThreads, v[u]);
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(const uint8_t* src, int src_pages, uint8_t* dst, int dst_pages, int layers, long long page_bytes,
+                int chunks, const int32_t* __restrict__ src_ids, const int32_t* __restrict__ dst_ids, int n,
+                int32_t* status) {
+  const long long items = (long long)n * layers * chunks;
+  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+    const int c = (int)(w % chunks);
+    const long long il = w / chunks;
+    const int l = (int)(il % layers), i = (int)(il / layers);
+    const int s = __ldg(src_ids + i), d = __ldg(dst_ids + i);
+    if (s == -1 || d == -1) continue;
+    if (s < 0 || s >= src_pages || d < 0 || d >= dst_pages) {
+      if (threadIdx.x == 0) report(status, SV_DEV_BAD_PAGE);
+      continue;
+    }
+    const long long off = (long long)c * kChunkBytes;
+    const int bytes = (int)min((long long)kChunkBytes, page_bytes - off);
+    copy_chunk(src + ((long long)l * src_pages + s) * page_bytes + off,
+               dst + ((long long)l * dst_pages + d) * page_bytes + off, bytes);
+  }
+}
+
+// The tails of forked requests: moves[i] = (page, its copy, rows).
+__global__ void __launch_bounds__(kCopyThreads)
+    fork_copy_kernel(uint8_t* pool, int P, int layers, long long row_bytes, int chunks, const int4* moves, int n) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long page_bytes = row_bytes * SV_PAGE_SIZE;
+  const long long items = (long long)n * layers * chunks;
+  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+    const int c = (int)(w % chunks);
+    const long long il = w / chunks;
+    const int l = (int)(il % layers), i = (int)(il / layers);
+    const int4 m = ld_dep_i4(moves + i);
+    const long long off = (long long)c * kChunkBytes, len = m.z * row_bytes;
+    if (off >= len) continue;
+    uint8_t* layer = pool + (long long)l * P * page_bytes;
+    copy_chunk(layer + m.x * page_bytes + off, layer + m.y * page_bytes + off,
+               (int)min((long long)kChunkBytes, len - off));
+  }
+}
+
+// The moves of a compaction, and the tables in the new numbering.
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_move_kernel(uint8_t* pool, int P, int layers, long long page_bytes, int chunks, const int* header,
+                        const int2* moves, const int32_t* table_in, int32_t* table_out,
+                        const int32_t* __restrict__ lens, int R, int mp, const int32_t* page_map, int32_t* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  constexpr int kWarps = kCopyThreads / 32;
+  for (int r = (int)blockIdx.x * kWarps + (threadIdx.x >> 5); r < R; r += (int)gridDim.x * kWarps) {
+    int len = __ldg(lens + r);
+    const int cap = mp * SV_PAGE_SIZE;
+    if (len < 0 || len > cap) {
+      if (lane == 0) report(status, SV_DEV_BAD_BOUND);
+      len = len < 0 ? 0 : cap;
+    }
+    const int held = (len + SV_PAGE_SIZE - 1) / SV_PAGE_SIZE;
+    for (int j = lane; j < mp; j += 32) {
+      const long long e = (long long)r * mp + j;
+      int p = table_in[e];
+      if (j < held) {
+        if (p < 0 || p >= P) {
+          report(status, SV_DEV_BAD_PAGE);
+        } else {
+          p = ld_dep_s32(page_map + p);
+          if (p < 0) report(status, SV_DEV_BAD_PAGE);
+        }
+      }
+      if (j < held || table_out != table_in) table_out[e] = p;
+    }
+  }
+  const long long items = (long long)ld_dep_s32(header + 1) * layers * chunks;
+  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+    const int c = (int)(w % chunks);
+    const long long il = w / chunks;
+    const int l = (int)(il % layers), i = (int)(il / layers);
+    const int src = ld_dep_s32(&moves[i].x), dst = ld_dep_s32(&moves[i].y);
+    const long long off = (long long)c * kChunkBytes;
+    uint8_t* layer = pool + (long long)l * P * page_bytes;
+    copy_chunk(layer + src * page_bytes + off, layer + dst * page_bytes + off,
+               (int)min((long long)kChunkBytes, page_bytes - off));
+  }
+}
+
+// ------------------------------------------------------------------ host side
+inline bool off_by(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct PagesLayout {
+  size_t header, claim, prefix, list, moves, live, total;
+};
+PagesLayout pages_layout(long long P, long long R, long long n) {
+  PagesLayout L;
+  const size_t rows = (size_t)(R > n ? R : n);
+  L.header = 0;
+  L.claim = 256;
+  L.prefix = L.claim + up256((size_t)R * 4);
+  L.list = L.prefix + up256(rows * 4);
+  L.moves = L.list + up256((size_t)P * 4);
+  L.live = L.moves + up256((size_t)(P * 8 > n * 16 ? P * 8 : n * 16));
+  L.total = L.live + up256((size_t)P * 8);
+  return L;
+}
+
+template <class Args>
+cudaError_t launch_meta(void (*kernel)(Args), const Args& a, long long words, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  const unsigned ctas = words <= kOneCtaWords ? 1 : kClusterMax;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kMetaThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+constexpr int kCopyCtas = 152 * 8;  // eight CTAs of 256 threads per SM
+
+template <class... Ts, class... Us>
+cudaError_t launch_dependent(void (*kernel)(Ts...), unsigned ctas, cudaStream_t st, Us... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Ts>(args)...);
+}
+
+inline unsigned copy_ctas(long long items) { return (unsigned)(items < kCopyCtas ? (items < 1 ? 1 : items) : kCopyCtas); }
+
+// The checks that the bookkeeping calls share.
+sv_status check_tables(int num_pages, int page_size, int R, int mp, const void* const* needed, int count) {
+  if (num_pages < 1 || R < 0 || mp < 0) return SV_ERR_SHAPE;
+  if (page_size != SV_PAGE_SIZE) return SV_ERR_UNSUPPORTED;
+  if ((long long)R * mp > 0x7FFFFFFFll || (long long)mp * SV_PAGE_SIZE > 0x7FFFFFFFll) return SV_ERR_SHAPE;
+  for (int i = 0; i < count; ++i)
+    if (!needed[i]) return SV_ERR_NULL;
+  for (int i = 0; i < count; ++i)
+    if (off_by(needed[i], 4)) return SV_ERR_ALIGN;
+  return SV_OK;
+}
+sv_status check_pool(const void* pool, int layers, size_t row_bytes) {
+  if (layers < 1 || row_bytes == 0 || row_bytes > (size_t)1 << 24) return SV_ERR_SHAPE;
+  if (row_bytes % 16 != 0) return SV_ERR_UNSUPPORTED;
+  if (!pool) return SV_ERR_NULL;
+  return off_by(pool, 16) ? SV_ERR_ALIGN : SV_OK;
+}
+sv_status check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need) return SV_ERR_WORKSPACE;
+  return off_by(ws, 256) ? SV_ERR_ALIGN : SV_OK;
+}
+inline sv_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return SV_OK;
+  cudaGetLastError();
+  return SV_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" size_t sv_kv_pages_workspace_bytes(int num_pages, int R, int n) {
+  if (num_pages < 0 || R < 0 || n < 0) return 256;
+  return sv::pages_layout(num_pages, R, n).total;
+}
+
+extern "C" sv_status kv_pages_copy(const void* src_pages, int src_num_pages, void* dst_pages, int dst_num_pages,
+                                   int layers, size_t page_bytes, const int32_t* src_ids, const int32_t* dst_ids,
+                                   int n, int32_t* status, sv_stream_t stream) {
+  using namespace sv;
+  if (src_num_pages < 0 || dst_num_pages < 0 || layers < 0 || n < 0) return SV_ERR_SHAPE;
+  if (page_bytes % 16 != 0 || page_bytes > (size_t)1 << 30) return SV_ERR_UNSUPPORTED;
+  if (n == 0 || layers == 0 || page_bytes == 0) return SV_OK;
+  if (!src_pages || !dst_pages || !src_ids || !dst_ids) return SV_ERR_NULL;
+  if (off_by(src_pages, 16) || off_by(dst_pages, 16) || off_by(src_ids, 4) || off_by(dst_ids, 4)) return SV_ERR_ALIGN;
+  const int chunks = (int)((page_bytes + kChunkBytes - 1) / kChunkBytes);
+  copy_kernel<<<copy_ctas((long long)n * layers * chunks), kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint8_t*>(src_pages), src_num_pages, static_cast<uint8_t*>(dst_pages), dst_num_pages, layers,
+      (long long)page_bytes, chunks, src_ids, dst_ids, n, status);
+  return launched(cudaGetLastError());
+}
+
+extern "C" sv_status kv_pages_resize(const int32_t* ref_counts_in, int num_pages, int page_size,
+                                     const int32_t* block_table_in, const int32_t* kv_lens_in, int R,
+                                     int max_pages_per_req, const int32_t* new_lens, int32_t* ref_counts_out,
+                                     int32_t* block_table_out, int32_t* kv_lens_out, void* workspace,
+                                     size_t workspace_bytes, int32_t* status, sv_stream_t stream) {
+  using namespace sv;
+  const void* needed[] = {ref_counts_in, ref_counts_out, block_table_in, block_table_out,
+                          kv_lens_in,    kv_lens_out,    new_lens};
+  const bool rows = R > 0 && max_pages_per_req > 0;
+  sv_status e = check_tables(num_pages, page_size, R, max_pages_per_req, needed, rows ? 7 : 2);
+  if (e != SV_OK) return e;
+  if (!rows && R > 0 && (!kv_lens_in || !kv_lens_out || !new_lens)) return SV_ERR_NULL;
+  e = check_workspace(workspace, workspace_bytes, sv_kv_pages_workspace_bytes(num_pages, R, 0));
+  if (e != SV_OK) return e;
+  const PagesLayout L = pages_layout(num_pages, R, 0);
+  char* ws = static_cast<char*>(workspace);
+  ResizeArgs a;
+  a.ref_in = ref_counts_in;
+  a.table_in = block_table_in;
+  a.lens_in = kv_lens_in;
+  a.new_lens = new_lens;
+  a.ref_out = ref_counts_out;
+  a.table_out = block_table_out;
+  a.lens_out = kv_lens_out;
+  a.status = status;
+  a.prefix = reinterpret_cast<int*>(ws + L.prefix);
+  a.list = reinterpret_cast<int*>(ws + L.list);
+  a.P = num_pages;
+  a.R = R;
+  a.mp = max_pages_per_req;
+  return launched(launch_meta(resize_kernel, a, num_pages + (long long)R * max_pages_per_req,
+                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" sv_status kv_pages_fork(void* kv_pages, int num_pages, int page_size, int layers, size_t row_bytes,
+                                   const int32_t* ref_counts_in, const int32_t* block_table_in,
+                                   const int32_t* kv_lens_in, int R, int max_pages_per_req, const int32_t* parents,
+                                   const int32_t* children, int n, int32_t* ref_counts_out, int32_t* block_table_out,
+                                   int32_t* kv_lens_out, void* workspace, size_t workspace_bytes, int32_t* status,
+                                   sv_stream_t stream) {
+  using namespace sv;
+  const void* needed[] = {ref_counts_in, ref_counts_out, block_table_in, block_table_out,
+                          kv_lens_in,    kv_lens_out,    parents,        children};
+  if (n < 0 || (n > 0 && (R < 1 || max_pages_per_req < 1))) return SV_ERR_SHAPE;
+  const bool rows = R > 0 && max_pages_per_req > 0;
+  sv_status e = check_tables(num_pages, page_size, R, max_pages_per_req, needed, rows ? (n > 0 ? 8 : 6) : 2);
+  if (e != SV_OK) return e;
+  if (!rows && R > 0 && (!kv_lens_in || !kv_lens_out)) return SV_ERR_NULL;
+  e = check_pool(kv_pages, layers, row_bytes);
+  if (e != SV_OK) return e;
+  e = check_workspace(workspace, workspace_bytes, sv_kv_pages_workspace_bytes(num_pages, R, n));
+  if (e != SV_OK) return e;
+  const PagesLayout L = pages_layout(num_pages, R, n);
+  char* ws = static_cast<char*>(workspace);
+  ForkArgs a;
+  a.ref_in = ref_counts_in;
+  a.table_in = block_table_in;
+  a.lens_in = kv_lens_in;
+  a.parents = parents;
+  a.children = children;
+  a.ref_out = ref_counts_out;
+  a.table_out = block_table_out;
+  a.lens_out = kv_lens_out;
+  a.status = status;
+  a.claim = reinterpret_cast<int*>(ws + L.claim);
+  a.prefix = reinterpret_cast<int*>(ws + L.prefix);
+  a.list = reinterpret_cast<int*>(ws + L.list);
+  a.moves = reinterpret_cast<int4*>(ws + L.moves);
+  a.P = num_pages;
+  a.R = R;
+  a.mp = max_pages_per_req;
+  a.n = n;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  e = launched(launch_meta(fork_kernel, a, num_pages + (long long)R * max_pages_per_req, st));
+  if (e != SV_OK || n == 0) return e;
+  const int chunks = (int)((row_bytes * SV_PAGE_SIZE + kChunkBytes - 1) / kChunkBytes);
+  return launched(launch_dependent(fork_copy_kernel, copy_ctas((long long)n * layers * chunks), st,
+                                   static_cast<uint8_t*>(kv_pages), num_pages, layers, (long long)row_bytes, chunks,
+                                   a.moves, n));
+}
+
+extern "C" sv_status kv_pages_compact(void* kv_pages, int num_pages, int page_size, int layers, size_t row_bytes,
+                                      const int32_t* ref_counts_in, const int32_t* block_table_in,
+                                      const int32_t* kv_lens, int R, int max_pages_per_req, int32_t* ref_counts_out,
+                                      int32_t* block_table_out, int32_t* page_map, int32_t* num_live, void* workspace,
+                                      size_t workspace_bytes, int32_t* status, sv_stream_t stream) {
+  using namespace sv;
+  const void* needed[] = {ref_counts_in, ref_counts_out, page_map, num_live, block_table_in, block_table_out, kv_lens};
+  const bool rows = R > 0 && max_pages_per_req > 0;
+  sv_status e = check_tables(num_pages, page_size, R, max_pages_per_req, needed, rows ? 7 : 4);
+  if (e != SV_OK) return e;
+  e = check_pool(kv_pages, layers, row_bytes);
+  if (e != SV_OK) return e;
+  e = check_workspace(workspace, workspace_bytes, sv_kv_pages_workspace_bytes(num_pages, R, 0));
+  if (e != SV_OK) return e;
+  const PagesLayout L = pages_layout(num_pages, R, 0);
+  char* ws = static_cast<char*>(workspace);
+  CompactArgs a;
+  a.ref_in = ref_counts_in;
+  a.ref_out = ref_counts_out;
+  a.page_map = page_map;
+  a.num_live = num_live;
+  a.live = reinterpret_cast<int2*>(ws + L.live);
+  a.holes = reinterpret_cast<int*>(ws + L.list);
+  a.header = reinterpret_cast<int*>(ws + L.header);
+  a.moves = reinterpret_cast<int2*>(ws + L.moves);
+  a.P = num_pages;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  e = launched(launch_meta(compact_kernel, a, num_pages, st));
+  if (e != SV_OK) return e;
+  const int chunks = (int)((row_bytes * SV_PAGE_SIZE + kChunkBytes - 1) / kChunkBytes);
+  const long long most = ((long long)num_pages / 2 + 1) * layers * chunks;
+  return launched(launch_dependent(compact_move_kernel, copy_ctas(most), st, static_cast<uint8_t*>(kv_pages), num_pages,
+                                   layers, (long long)(row_bytes * SV_PAGE_SIZE), chunks, a.header, a.moves,
+                                   block_table_in, block_table_out, kv_lens, rows ? R : 0, max_pages_per_req, page_map,
+                                   status));
+}

@@ -1,0 +1,351 @@
+"""kv_pages_copy, kv_pages_fork, kv_pages_resize and kv_pages_compact against
+their sequential oracle, bit for bit: pool sizes on both sides of the tile and
+cluster borders, shared pages, full pools, bad device data, updates in place
+and out of place, captured and replayed calls, and a run of all of them."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verify_mla_gb300 as m
+    m.load_library()
+    return m
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def i32(x):
+    return dev(np.asarray(x, dtype=np.int32))
+
+
+def make_state(rng, P, R, mp, share=True, empty=0.2, full_len=None):
+    """Requests over scattered pages, some empty, some sharing a prefix of full pages."""
+    order = rng.permutation(P)
+    refs, table, lens = np.zeros(P, np.int32), rng.integers(-9, P + 9, (R, mp)).astype(np.int32), np.zeros(R, np.int32)
+    used = 0
+    for r in range(R):
+        if rng.random() < empty:
+            continue
+        n = int(rng.integers(1, mp * 64 + 1)) if full_len is None else full_len
+        k = -(-n // 64)
+        shared = 0
+        if share and r and lens[r - 1] and rng.random() < 0.5:
+            shared = int(rng.integers(0, min(n, int(lens[r - 1])) // 64 + 1))
+        if used + k - shared > P:
+            continue
+        table[r, :shared] = table[r - 1, :shared]
+        table[r, shared:k] = order[used:used + k - shared]
+        used += k - shared
+        refs[table[r, :k]] += 1
+        lens[r] = n
+    return refs, table, lens
+
+
+def make_pool(rng, L, P, width=32):
+    return rng.integers(0, 256, (L, P, 64, width)).astype(np.uint8)
+
+
+def check(got, want):
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy(), np.asarray(w)), (g.cpu().numpy(), w)
+
+
+# one CTA (P + R mp <= 16384), one tile of eight CTAs, several tiles
+SHAPES = [(1, 1, 1), (7, 3, 2), (300, 9, 24), (8192, 40, 33), (16000, 5, 70), (20000, 64, 100), (70001, 130, 300), (140000, 33, 40)]
+
+
+@pytest.mark.parametrize("P,R,mp", SHAPES)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_resize(sv, P, R, mp, in_place):
+    rng = np.random.default_rng(P + R + mp + in_place)
+    for case in range(3):
+        refs, table, lens = make_state(rng, P, R, mp)
+        new = np.where(rng.random(R) < 0.5, np.clip(lens + rng.integers(-70, 140, R), 0, mp * 64), rng.integers(0, mp * 64 + 1, R))
+        new[rng.random(R) < 0.1] = -1
+        new[rng.random(R) < 0.1] = 0
+        if case == 2:  # everything given back
+            new[:] = 0
+        want = oracle.ref_pages_resize(refs, table, lens, new.astype(np.int32))
+        a, b, c, st = i32(refs), i32(table), i32(lens), i32([0])
+        outs = dict(ref_counts_out=a, block_table_out=b, kv_lens_out=c) if in_place else {}
+        got = sv.kv_pages_resize(a, b, c, i32(new), status=st, **outs)
+        check((*got, st), (*want[:3], [want[3]]))
+        if not in_place:
+            check((a, b, c), (refs, table, lens))
+
+
+def test_resize_bad_data(sv):
+    """Lengths out of range, entries outside the pool or of free pages, a full
+    pool: reported, left undone for that request, the others served."""
+    rng = np.random.default_rng(3)
+    P, R, mp = 200, 12, 10
+    for case in range(6):
+        refs, table, lens = make_state(rng, P, R, mp, share=True, empty=0.3)
+        new = np.clip(lens + rng.integers(-200, 200, R), 0, mp * 64).astype(np.int32)
+        if case == 0:
+            lens[3], lens[4], new[5], new[6] = -5, mp * 64 + 1, mp * 64 + 1, -2
+        elif case == 1:
+            table[2, 0], lens[2], new[2] = P, 40, 0
+            table[5, 1], lens[5], new[5] = -3, 100, 64
+        elif case == 2:
+            table[7, :2], lens[7], new[7] = np.flatnonzero(refs == 0)[0], 128, 0  # a free page, twice
+        elif case == 3:
+            refs[refs == 0] = 1  # full: only what is given back can be had
+        elif case == 4:
+            refs[:] = 1
+            new = np.minimum(np.maximum(lens, new), mp * 64).astype(np.int32)
+        else:
+            table[1, 0], lens[1], new[1] = P + 3, 10, 30  # grows inside an entry that is no page
+        want = oracle.ref_pages_resize(refs, table, lens, new)
+        st = i32([0])
+        got = sv.kv_pages_resize(i32(refs), i32(table), i32(lens), i32(new), status=st)
+        check((*got, st), (*want[:3], [want[3]]))
+        sv.kv_pages_resize(i32(refs), i32(table), i32(lens), i32(new))  # without a status word
+
+
+@pytest.mark.parametrize("P,R,mp,n,L,width", [(7, 3, 2, 2, 1, 512), (300, 30, 24, 20, 3, 32), (300, 30, 24, 30, 1, 1024),
+                                              (20000, 64, 100, 50, 1, 16), (70001, 130, 30, 129, 1, 16), (500, 3000, 2, 2500, 1, 48)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_fork(sv, P, R, mp, n, L, width, in_place):
+    rng = np.random.default_rng(P + n + in_place)
+    refs, table, lens = make_state(rng, P, R, mp, empty=0.6)
+    lens[rng.integers(0, R)] = 0
+    held, empty = np.flatnonzero(lens), np.flatnonzero(lens == 0)
+    parents = rng.choice(held, n) if len(held) else np.zeros(n, np.int64)
+    children = np.resize(rng.permutation(empty), n)  # named twice where there are too few
+    pool = make_pool(rng, L, P, width)
+    want = oracle.ref_pages_fork(pool, refs, table, lens, parents, children)
+    a, b, c, st, kv = i32(refs), i32(table), i32(lens), i32([0]), dev(pool)
+    outs = dict(ref_counts_out=a, block_table_out=b, kv_lens_out=c) if in_place else {}
+    got = sv.kv_pages_fork(kv, a, b, c, i32(parents), i32(children), status=st, **outs)
+    check((kv, *got, st), (*want[:4], [want[4]]))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_fork_bad_data(sv, in_place):
+    """Bad indices, children in use or named twice, a child that is a parent,
+    lengths out of range, entries outside the pool, no page left."""
+    rng = np.random.default_rng(5)
+    P, R, mp = 60, 12, 5
+    for case in range(5):
+        refs, table, lens = make_state(rng, P, R, mp, share=False, empty=0.0, full_len=100)
+        for r in range(4, R):  # requests 4.. hold nothing
+            refs[table[r, :2]] = 0
+            lens[r] = 0
+        parents, children = np.array([0, 1, 2, 3, 0, 1]), np.array([4, 5, 6, 7, 8, 9])
+        if case == 0:
+            parents[1], children[2], parents[3], children[4] = -1, R, R, -1
+        elif case == 1:
+            children[1], children[3], parents[5] = 4, 4, 4  # named again; a parent that becomes a child in this call
+        elif case == 2:
+            children[0] = 3  # in use
+            lens[1], lens[2] = mp * 64 + 1, -1
+        elif case == 3:
+            table[0, 0], table[1, 1], table[2, 0] = P, -2, -1
+        else:
+            refs[refs == 0] = 1
+            refs[[7, 9]] = 0
+            lens[3] = 64  # a request without a tail still forks
+        pool = make_pool(rng, 2, P, 16)
+        want = oracle.ref_pages_fork(pool, refs, table, lens, parents, children)
+        a, b, c, st, kv = i32(refs), i32(table), i32(lens), i32([0]), dev(pool)
+        outs = dict(ref_counts_out=a, block_table_out=b, kv_lens_out=c) if in_place else {}
+        got = sv.kv_pages_fork(kv, a, b, c, i32(parents), i32(children), status=st, **outs)
+        check((kv, *got, st), (*want[:4], [want[4]]))
+
+
+@pytest.mark.parametrize("P,R,mp,L,width", [(1, 1, 1, 1, 16), (7, 3, 2, 2, 512), (300, 9, 24, 2, 1024), (20000, 64, 100, 1, 16),
+                                            (70001, 130, 300, 1, 16), (140000, 33, 40, 1, 16)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact(sv, P, R, mp, L, width, in_place):
+    rng = np.random.default_rng(P + L + in_place)
+    refs, table, lens = make_state(rng, P, R, mp)
+    pool = make_pool(rng, L, P, width)
+    want = oracle.ref_pages_compact(pool, refs, table, lens)
+    a, b, c, st, kv = i32(refs), i32(table), i32(lens), i32([0]), dev(pool)
+    outs = dict(ref_counts_out=a, block_table_out=b) if in_place else {}
+    got = sv.kv_pages_compact(kv, a, b, c, status=st, **outs)
+    check((kv, *got, st), (*want[:4], [want[4]], [want[5]]))
+
+
+@pytest.mark.parametrize("fill", ["none", "all", "front", "back"])
+def test_compact_extremes(sv, fill):
+    rng = np.random.default_rng(8)
+    P = 100
+    refs = np.zeros(P, np.int32)
+    refs[{"none": slice(0, 0), "all": slice(0, P), "front": slice(0, 40), "back": slice(60, P)}[fill]] = 3
+    table = rng.integers(-2, P + 2, (5, 4)).astype(np.int32)  # free pages and ids outside the pool among the entries
+    lens = np.array([0, 256, 100, 257, -1], np.int32)
+    pool = make_pool(rng, 1, P, 16)
+    want = oracle.ref_pages_compact(pool, refs, table, lens)
+    st, kv = i32([0]), dev(pool)
+    got = sv.kv_pages_compact(kv, i32(refs), i32(table), i32(lens), status=st)
+    check((kv, *got, st), (*want[:4], [want[4]], [want[5]]))
+
+
+@pytest.mark.parametrize("L,P,n,width,dtype", [(1, 2, 1, 16, torch.uint8), (1, 64, 20, 512, torch.bfloat16), (3, 50, 25, 512, torch.uint8),
+                                               (5, 33, 9, 24, torch.bfloat16), (2, 300, 150, 512, torch.bfloat16)])
+@pytest.mark.parametrize("same", [False, True])
+def test_copy(sv, L, P, n, width, dtype, same):
+    rng = np.random.default_rng(P + n)
+    bytes_ = width * torch.empty(0, dtype=dtype).element_size()
+    src = make_pool(rng, L, P, bytes_)
+    dst = src if same else make_pool(rng, L, P + 3, bytes_)
+    ids = rng.permutation(P)
+    s, d = ids[:n].copy(), ids[P - n:].copy() if same else rng.permutation(P + 3)[:n]
+    if n > 4:
+        s[1], d[2], s[3], d[4] = -1, -1, P, -2  # skipped, skipped, outside, outside
+    want, status = oracle.ref_pages_copy(src, dst, s, d)
+    st = i32([0])
+    as_pool = lambda x: dev(x).view(dtype) if L > 1 else dev(x[0]).view(dtype)  # noqa: E731
+    a = as_pool(src)
+    b = a if same else as_pool(dst)
+    out = sv.kv_pages_copy(a, b, i32(s), i32(d), status=st)
+    assert out is b and int(st.item()) == status
+    assert np.array_equal(b.view(torch.uint8).cpu().numpy().reshape(want.shape), want)
+
+
+def test_empty_calls(sv):
+    pool, none = torch.zeros((4, 64, 512), dtype=torch.bfloat16, device=DEV), i32(np.zeros(0))
+    sv.kv_pages_copy(pool, pool, none, none)
+    refs = i32([1, 0, 2, 0])
+    for R, mp in ((0, 3), (2, 0)):
+        table, lens = torch.zeros((R, mp), dtype=torch.int32, device=DEV), i32(np.zeros(R))
+        got = sv.kv_pages_resize(refs, table, lens, lens)
+        assert torch.equal(got[0], refs) and torch.equal(got[2], lens)
+        got = sv.kv_pages_fork(pool, refs, table, lens, none, none)
+        assert torch.equal(got[0], refs) and torch.equal(got[2], lens)
+        got = sv.kv_pages_compact(pool, refs, table, lens)
+        check(got[0:1] + got[2:], ([1, 2, 0, 0], [0, -1, 1, -1], [2]))
+
+
+def test_refusals(sv):
+    refs, table, lens = i32(np.zeros(8)), i32(np.zeros((2, 3))), i32([0, 0])
+    pool = torch.zeros((8, 64, 512), dtype=torch.bfloat16, device=DEV)
+    for bad in (dict(ref_counts=refs.long()), dict(block_table=i32(np.zeros((3, 2))).t()), dict(kv_lens=i32([0])),
+                dict(new_lens=i32([0, 0, 0])), dict(kv_lens=lens.cpu()), dict(workspace=torch.empty(300, dtype=torch.uint8)),
+                dict(kv_lens_out=i32([0])), dict(status=torch.zeros(1, device=DEV))):
+        args = dict(ref_counts=refs, block_table=table, kv_lens=lens, new_lens=lens) | bad
+        with pytest.raises(ValueError):
+            sv.kv_pages_resize(**args)
+    with pytest.raises(sv.SpecVerifyError):
+        sv.kv_pages_resize(refs, table, lens, lens, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        sv.kv_pages_fork(pool[:7], refs, table, lens, lens, lens)
+    with pytest.raises(ValueError):
+        sv.kv_pages_compact(pool.transpose(0, 1), refs, table, lens)
+    with pytest.raises(ValueError):
+        sv.kv_pages_copy(pool, pool.float(), lens, lens)
+    with pytest.raises(sv.SpecVerifyError):
+        odd = torch.zeros((8, 64, 12), dtype=torch.uint8, device=DEV)
+        sv.kv_pages_fork(odd, refs, table, lens, lens, lens)  # rows of 12 bytes
+
+
+def test_streams_and_graph(sv):
+    """Captured calls replay on new contents of their buffers; two captured
+    graphs with workspaces of their own run beside each other."""
+    rng = np.random.default_rng(11)
+    P, R, mp = 20000, 40, 60
+    states = [make_state(rng, P, R, mp) for _ in range(3)]
+    news = [np.clip(s[2] + rng.integers(-100, 100, R), 0, mp * 64).astype(np.int32) for s in states]
+    graphs = []
+    for k in range(2):
+        bufs = [i32(x) for x in (*states[k], news[k])]
+        outs = [torch.empty_like(b) for b in bufs[:3]]
+        ws = torch.empty(sv.kv_pages_workspace_bytes(P, R), dtype=torch.uint8, device=DEV)
+        st = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            sv.kv_pages_resize(*bufs, *outs, workspace=ws)
+        graphs.append((g, st, bufs, outs, ws))
+    for turn in range(3):
+        for k, (g, st, bufs, outs, ws) in enumerate(graphs):
+            x = (turn + k) % 3
+            for b, v in zip(bufs, (*states[x], news[x])):
+                b.copy_(i32(v))
+        torch.cuda.synchronize()
+        for g, st, bufs, outs, ws in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for k, (g, st, bufs, outs, ws) in enumerate(graphs):
+            x = (turn + k) % 3
+            check(outs, oracle.ref_pages_resize(*states[x], news[x])[:3])
+
+
+def test_a_cache_through_its_life(sv):
+    """Admit, append, fork, append to both, drop the rejected tails, finish
+    some, compact, move to another pool: what a request's attention reads
+    stays what was appended to it."""
+    rng = np.random.default_rng(21)
+    P, R, mp, L = 90, 10, 8, 2
+    refs, table, lens = i32(np.zeros(P)), i32(np.full((R, mp), -1)), i32(np.zeros(R))
+    pool = torch.zeros((L, P, 64, 512), dtype=torch.bfloat16, device=DEV)
+    status = i32([0])
+    truth = [np.zeros((0, 512), np.float32) for _ in range(R)]
+
+    def resize(new):
+        sv.kv_pages_resize(refs, table, lens, i32(new), refs, table, lens, status=status)
+
+    def append(k, on):
+        resize([len(truth[r]) + (k if r in on else 0) for r in range(R)])
+        rows = torch.randn((R, k, 512), device=DEV).bfloat16()
+        pos = np.full((R, k), -1, np.int32)
+        for r in on:
+            pos[r] = np.arange(len(truth[r]), len(truth[r]) + k)
+            truth[r] = np.concatenate([truth[r], rows[r].float().cpu().numpy()])
+        for layer in range(L):
+            sv.mla_kv_append((rows * (layer + 1)).reshape(-1, 512), i32(pos.reshape(-1)), table, pool[layer], k, status=status)
+
+    def same():
+        t, n, p = table.cpu().numpy(), lens.cpu().numpy(), pool.float().cpu().numpy()
+        held = np.concatenate([t[r, :-(-int(n[r]) // 64)] for r in range(R)]).astype(int)
+        assert np.array_equal(np.bincount(held, minlength=P), refs.cpu().numpy())
+        for r in range(R):
+            assert n[r] == len(truth[r])
+            for layer in range(L):
+                rows = p[layer][t[r, :-(-int(n[r]) // 64)]].reshape(-1, 512)[:n[r]]
+                assert np.array_equal(rows, truth[r] * (layer + 1)), (r, layer)
+
+    def cut(lengths):
+        for r, n in enumerate(lengths):
+            truth[r] = truth[r][:n]
+        resize([len(x) for x in truth])
+
+    append(100, [0, 1])
+    append(64, [2])
+    same()
+    sv.kv_pages_fork(pool, refs, table, lens, i32([0, 0, 2, 1]), i32([5, 6, 7, 8]), refs, table, lens, status=status)
+    for a, b in ((0, 5), (0, 6), (2, 7), (1, 8)):
+        truth[b] = truth[a].copy()
+    same()
+    append(50, [0, 2, 5, 6, 7, 8])
+    same()
+    cut([len(x) - 3 if len(x) > 10 else len(x) for x in truth])
+    same()
+    cut([0 if r in (0, 2, 8) else len(x) for r, x in enumerate(truth)])
+    append(130, [9])
+    same()
+    out = sv.kv_pages_compact(pool, refs, table, lens, refs, table, status=status)
+    assert int(out[3].item()) == int((refs > 0).sum().item())
+    same()
+    other = torch.zeros_like(pool)
+    live = torch.arange(int(out[3].item()), dtype=torch.int32, device=DEV)
+    sv.kv_pages_copy(pool, other, live, live, status=status)
+    pool = other
+    same()
+    append(9, [1, 5, 9])
+    same()
+    assert int(status.item()) == 0
