@@ -16,6 +16,7 @@
  *   mla_wuv_project     the per-head W_UV value up-projection after the merge.
  *   mla_kv_append       the verify tokens' latent rows into the paged cache.
  *   spec_verify_sampled rejection-sampling verification (probabilistic drafts).
+ *   sample_tokens       tokens drawn under temperature, top-k, top-p and min-p.
  *   kv_pages_copy       pages of one pool into pages of another or the same.
  *   kv_pages_fork       requests continued from another's cache, sharing pages.
  *   kv_pages_resize     the pages of new lengths, handed out and taken back.
@@ -74,6 +75,10 @@ typedef enum {
 #define SV_DEV_SHARED_PAGE 0x10 /* a request would grow inside a page that others hold too */
 #define SV_DEV_NO_PAGE     0x20 /* the pool has too few free pages                         */
 #define SV_DEV_BAD_REQUEST 0x40 /* a request index out of range, or a child that is in use */
+/* sample_tokens */
+#define SV_DEV_BAD_LOGITS  0x80 /* a row with no finite largest logit, or no temperature       */
+#define SV_LOGITS_F32 0
+#define SV_LOGITS_BF16 1
 
 #define SV_LATENT_DIM 512
 #define SV_PAGE_SIZE 64
@@ -505,6 +510,52 @@ sv_status spec_verify_sampled(const float* logits, int R, int k, int V, float te
                               const float* uniforms, const int32_t* kv_lens_in,
                               int32_t* accepted, int32_t* next_tokens, int32_t* kv_lens_out,
                               void* workspace, size_t workspace_bytes, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * sample_tokens
+ *
+ * One token per row of logits under a temperature, top-k, top-p and min-p,
+ * from the caller's random numbers; with probs, also the distribution that it
+ * was drawn from (the draft_probs row of spec_verify_sampled for a drafted
+ * token).  For row t with logits x, m = max x, tau = temperature:
+ *     w_v = exp((x_v - m) / tau); tokens with w_v < 2^-40 are left out
+ *     top-k keeps x_v >= the top_k-th largest logit  (top_k <= 0 or > V: all)
+ *     top-p keeps x_v >= the largest logit s such that the tokens of top-k with
+ *           x >= s hold at least the share top_p of the weight of top-k
+ *           (top_p >= 1: all;  top_p <= 0: the largest logit)
+ *     min-p keeps w_v >= min_p  (min_p <= 0: all;  min_p >= 1: the largest)
+ *     tokens[t] = the smallest v with
+ *           sum_{i <= v, kept} w_i > uniforms[t] * sum_{kept} w_i
+ *     probs[t][v] = w_v / sum_{kept} w_i where v is kept, else 0
+ * Ties at a border are all kept.  A temperature <= 0 (or below 2^-64) takes
+ * the lowest index of the largest logit, probs one-hot.
+ *
+ * A logit of -inf (or NaN) masks its token.  A row without a finite largest
+ * logit (all masked, or +inf), or with a temperature that is NaN or +inf,
+ * gets token -1, probs all 0 and sets SV_DEV_BAD_LOGITS.  A uniform outside
+ * [0, 1) counts as the nearest value in it (NaN: 0), a NaN top_p or min_p as
+ * off.
+ *
+ * Weights are fixed-point integers (relative error below 2^-30, unit
+ * 2^-(62 - ceil(log2 V)) of the largest) and every sum is a 64-bit integer sum,
+ * so the token does not depend on the order of summation and differs from
+ * exact arithmetic only where a border lies within about 1e-8 of the total.
+ *
+ *   logits       [T][V] of logits_type SV_LOGITS_F32 or SV_LOGITS_BF16, rows
+ *                row_stride >= V elements apart, aligned to its element.
+ *   V            1 .. 2^22 (else SV_ERR_UNSUPPORTED above).
+ *   uniforms     fp32 [T].
+ *   temperature, top_k, top_p, min_p   device arrays [T] (fp32, int32, fp32,
+ *                fp32), or NULL to take the *_all value for every row.
+ *   tokens       int32 [T];  probs fp32 [T][V], may be NULL.
+ *   status       device int32, may be NULL.
+ * No workspace; one kernel on `stream`.
+ * ---------------------------------------------------------------------- */
+sv_status sample_tokens(const void* logits, int logits_type, int T, int V, long long row_stride,
+                        const float* uniforms, const float* temperature, float temperature_all,
+                        const int32_t* top_k, int top_k_all, const float* top_p, float top_p_all,
+                        const float* min_p, float min_p_all, int32_t* tokens, float* probs,
+                        int32_t* status, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * spec_verify_greedy_noalloc

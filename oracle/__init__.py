@@ -15,3 +15,4 @@ from .verify_ref import (  # noqa: F401
 )
 from .sampled_ref import inverse_cdf, ref_sampled_verify, target_probs  # noqa: F401
 from .pages_ref import ref_pages_compact, ref_pages_copy, ref_pages_fork, ref_pages_resize  # noqa: F401
+from .sample_ref import ref_sample_row, ref_sample_tokens  # noqa: F401

@@ -6,6 +6,7 @@ The compute lives in ``libspecverify.so`` (hand-written sm_103a CUDA, C ABI in
 from .binding import (  # noqa: F401
     EXPORTED_SYMBOLS,
     SV_DEV_BAD_BOUND,
+    SV_DEV_BAD_LOGITS,
     SV_DEV_BAD_PAGE,
     SV_DEV_BAD_REQUEST,
     SV_DEV_NO_PAGE,
@@ -31,6 +32,7 @@ from .binding import (  # noqa: F401
     mla_verify_decode,
     mla_wuv_project,
     num_splits_for,
+    sample_tokens,
     sampled_workspace,
     sampled_workspace_bytes,
     spec_verify_greedy,

@@ -35,6 +35,7 @@ SV_DEV_TIMEOUT = 0x4
 SV_DEV_SHARED_PAGE = 0x10
 SV_DEV_NO_PAGE = 0x20
 SV_DEV_BAD_REQUEST = 0x40
+SV_DEV_BAD_LOGITS = 0x80
 
 EXPORTED_SYMBOLS = (
     "sv_status_string",
@@ -55,6 +56,7 @@ EXPORTED_SYMBOLS = (
     "kv_pages_fork",
     "kv_pages_resize",
     "kv_pages_compact",
+    "sample_tokens",
 )
 
 _lib = None
@@ -134,6 +136,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.kv_pages_resize.restype = i
         lib.kv_pages_compact.argtypes = [p, i, i, i, z, p, p, p, i, i, p, p, p, p, p, z, p, p]
         lib.kv_pages_compact.restype = i
+        f = _c_float
+        lib.sample_tokens.argtypes = [p, i, i, i, ctypes.c_longlong, p, p, f, p, i, p, f, p, f, p, p, p, p]
+        lib.sample_tokens.restype = i
         _lib = lib
         return lib
 
@@ -555,3 +560,54 @@ def kv_pages_compact(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_tab
                                     ws.numel() * ws.element_size(), _ptr(status), _stream(dev))
     _check_status("kv_pages_compact", code)
     return (*outs, num_live)
+
+
+# ------------------------------------------------------------------ sampling
+_LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _setting(name: str, v, dtype: torch.dtype, T: int, dev: torch.device):
+    """(pointer, value) of a setting that is one number or a tensor [T]."""
+    if not isinstance(v, torch.Tensor):
+        return None, v
+    _check(v.dtype == dtype and v.device == dev and v.is_contiguous() and tuple(v.shape) == (T,),
+           f"{name}: a number, or {dtype}, contiguous, [T] on {dev}")
+    return v.data_ptr(), 0
+
+
+def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                  return_probs: bool = False, tokens: torch.Tensor | None = None, probs: torch.Tensor | None = None,
+                  status: torch.Tensor | None = None):
+    """Draw a token per row of logits [T, V] (fp32 or bf16, rows may be strided)
+    under a temperature, top-k, top-p and min-p, each one number or a tensor
+    [T] (int32 for top_k, else fp32), from uniforms [T] fp32 in [0, 1).
+    Returns tokens [T] int32 or, with return_probs or a probs tensor,
+    (tokens, probs [T, V] fp32): the distribution the token was drawn from."""
+    lib = load_library()
+    _check(logits.dim() == 2 and logits.dtype in _LOGITS_TYPES, "logits must be [T, V], fp32 or bf16")
+    dev = logits.device
+    _check(dev.type == "cuda", "tensors must live on a CUDA device")
+    T, V = logits.shape
+    _check(V == 1 or logits.stride(1) == 1, "a row of logits must be contiguous")
+    _check(uniforms.dtype == torch.float32 and uniforms.device == dev and uniforms.is_contiguous()
+           and tuple(uniforms.shape) == (T,), f"uniforms: fp32, contiguous, [T] on {dev}")
+    settings = (*_setting("temperature", temperature, torch.float32, T, dev), *_setting("top_k", top_k, torch.int32, T, dev),
+                *_setting("top_p", top_p, torch.float32, T, dev), *_setting("min_p", min_p, torch.float32, T, dev))
+    if tokens is None:
+        tokens = torch.empty(T, dtype=torch.int32, device=dev)
+    else:
+        _ints(dev, tokens=tokens)
+        _check(tuple(tokens.shape) == (T,), "tokens must be [T]")
+    if probs is not None:
+        _check(probs.dtype == torch.float32 and probs.device == dev and probs.is_contiguous()
+               and tuple(probs.shape) == (T, V), f"probs: fp32, contiguous, [T, V] on {dev}")
+    elif return_probs:
+        probs = torch.empty((T, V), dtype=torch.float32, device=dev)
+    _status_ok(status, dev)
+    stride = logits.stride(0) if T > 1 else V
+    _check(stride >= V, "rows of logits must not overlap")
+    with _on_device(dev):
+        code = lib.sample_tokens(logits.data_ptr(), _LOGITS_TYPES[logits.dtype], T, V, stride, uniforms.data_ptr(),
+                                 *settings, tokens.data_ptr(), _ptr(probs), _ptr(status), _stream(dev))
+    _check_status("sample_tokens", code)
+    return tokens if probs is None else (tokens, probs)
