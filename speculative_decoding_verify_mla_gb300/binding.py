@@ -8,8 +8,8 @@ is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -152,7 +152,8 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _check(cond: bool, msg: str):
@@ -406,60 +407,83 @@ def mla_wuv_project(x: torch.Tensor, w_uv: torch.Tensor, out_v: torch.Tensor | N
 
 
 # ------------------------------------------------------------------ pages of the cache
-def _on_device(dev: torch.device):
-    """The launch goes to the current device: make it the tensors' own."""
+# The calls below are short on the GPU (2 to 20 us), so their host time
+# counts: messages are built only where a check fails.
+_INT32, _FP32 = torch.int32, torch.float32
+
+
+def _launch(func: str, dev: torch.device, *args):
+    """Call the library with the tensors' device current (launches go there)."""
+    f = getattr(load_library(), func)
     if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        code = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, _stream(dev))
+    if code != 0:
+        raise SpecVerifyError(func, code)
 
 
+def _vector(name: str, t: torch.Tensor, dtype: torch.dtype, dev: torch.device, n: int):
+    if t.dtype is not dtype or t.device != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {dtype}, contiguous, [{n}] on {dev}")
+    return t.data_ptr()
+
+
+def _result(name: str, out: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty_like(like)
+    if out.dtype is not like.dtype or out.device != like.device or out.shape != like.shape or not out.is_contiguous():
+        raise ValueError(f"{name}: {like.dtype}, contiguous, {tuple(like.shape)} on {like.device}")
+    return out
+
+
+def _status_ptr(status: torch.Tensor | None, dev: torch.device):
+    if status is None:
+        return None
+    if status.dtype is not _INT32 or status.device != dev or status.numel() < 1:
+        raise ValueError(f"status: int32 on {dev}")
+    return status.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
 def kv_pages_workspace_bytes(num_pages: int, R: int, n: int = 0) -> int:
     """Workspace of a kv_pages_* call over a pool of num_pages pages and R
     requests (n: forks of a kv_pages_fork call)."""
     return int(load_library().sv_kv_pages_workspace_bytes(num_pages, R, n))
 
 
-def _pool_shape(name: str, t: torch.Tensor):
-    """(layers, pages, bytes of a row) of [P, 64, W] or [layers, P, 64, W]."""
-    _check(t.device.type == "cuda", "tensors must live on a CUDA device")
-    _check(t.dim() in (3, 4) and t.shape[-2] == SV_PAGE_SIZE and t.is_contiguous(),
-           f"{name} must be contiguous, [P, 64, W] or [layers, P, 64, W]")
-    return (t.shape[0] if t.dim() == 4 else 1), t.shape[-3], t.shape[-1] * t.element_size()
-
-
-def _ints(dev: torch.device, **tensors):
-    for name, t in tensors.items():
-        _check(t.dtype == torch.int32 and t.device == dev and t.is_contiguous(), f"{name}: int32, contiguous, on {dev}")
-
-
-def _like(name: str, out: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
-    if out is None:
-        return torch.empty_like(like)
-    _check(out.dtype == like.dtype and out.device == like.device and out.shape == like.shape and out.is_contiguous(),
-           f"{name}: {like.dtype}, contiguous, {tuple(like.shape)} on {like.device}")
-    return out
-
-
-def _status_ok(status: torch.Tensor | None, dev: torch.device):
-    if status is not None:
-        _check(status.dtype == torch.int32 and status.device == dev and status.numel() >= 1, f"status: int32 on {dev}")
-
-
 def _pages_workspace(dev: torch.device, workspace: torch.Tensor | None, need: int) -> torch.Tensor:
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous, on {dev}")
     return workspace
 
 
+def _pool_shape(name: str, t: torch.Tensor):
+    """(layers, pages, bytes of a row) of [P, 64, W] or [layers, P, 64, W]."""
+    shape = t.shape
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if len(shape) not in (3, 4) or shape[-2] != SV_PAGE_SIZE or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, [P, 64, W] or [layers, P, 64, W]")
+    return (shape[0] if len(shape) == 4 else 1), shape[-3], shape[-1] * t.element_size()
+
+
 def _tables(ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor):
+    """(device, P, R, max_pages, the three pointers)"""
     dev = ref_counts.device
-    _check(dev.type == "cuda", "tensors must live on a CUDA device")
-    _ints(dev, ref_counts=ref_counts, block_table=block_table, kv_lens=kv_lens)
-    _check(ref_counts.dim() == 1, "ref_counts must be [P]")
-    _check(block_table.dim() == 2, "block_table must be [R, max_pages]")
-    _check(kv_lens.shape == block_table.shape[:1], "kv_lens must be [R]")
-    return dev, ref_counts.shape[0], block_table.shape[0], block_table.shape[1]
+    if not ref_counts.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if ref_counts.dim() != 1:
+        raise ValueError("ref_counts must be [P]")
+    P = ref_counts.shape[0]
+    refs = _vector("ref_counts", ref_counts, _INT32, dev, P)
+    if block_table.dtype is not _INT32 or block_table.device != dev or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError(f"block_table: int32, contiguous, [R, max_pages] on {dev}")
+    R, max_pages = block_table.shape
+    return dev, P, R, max_pages, (refs, block_table.data_ptr(), _vector("kv_lens", kv_lens, _INT32, dev, R))
 
 
 def kv_pages_copy(src_pages: torch.Tensor, dst_pages: torch.Tensor, src_ids: torch.Tensor, dst_ids: torch.Tensor,
@@ -468,20 +492,17 @@ def kv_pages_copy(src_pages: torch.Tensor, dst_pages: torch.Tensor, src_ids: tor
     (in place), in every layer.  The pools are [P, 64, W] or [layers, P, 64, W]
     and may be one tensor; an id of -1 skips the pair.  Destinations must be
     distinct and, in one pool, no source of the call."""
-    lib = load_library()
     layers, src_p, row = _pool_shape("src_pages", src_pages)
     dst_layers, dst_p, dst_row = _pool_shape("dst_pages", dst_pages)
     dev = dst_pages.device
-    _check(src_pages.device == dev, f"src_pages must be on {dev}")
-    _check(src_pages.dtype == dst_pages.dtype and layers == dst_layers and row == dst_row,
-           "the pools must have the same type, layers and row width")
-    _ints(dev, src_ids=src_ids, dst_ids=dst_ids)
-    _check(src_ids.dim() == 1 and src_ids.shape == dst_ids.shape, "src_ids and dst_ids must be [n]")
-    _status_ok(status, dev)
-    with _on_device(dev):
-        code = lib.kv_pages_copy(_ptr(src_pages), src_p, _ptr(dst_pages), dst_p, layers, row * SV_PAGE_SIZE,
-                                 _ptr(src_ids), _ptr(dst_ids), src_ids.shape[0], _ptr(status), _stream(dev))
-    _check_status("kv_pages_copy", code)
+    if src_pages.device != dev:
+        raise ValueError(f"src_pages must be on {dev}")
+    if src_pages.dtype is not dst_pages.dtype or layers != dst_layers or row != dst_row:
+        raise ValueError("the pools must have the same type, layers and row width")
+    n = src_ids.numel()
+    _launch("kv_pages_copy", dev, src_pages.data_ptr(), src_p, dst_pages.data_ptr(), dst_p, layers, row * SV_PAGE_SIZE,
+            _vector("src_ids", src_ids, _INT32, dev, n), _vector("dst_ids", dst_ids, _INT32, dev, n), n,
+            _status_ptr(status, dev))
     return dst_pages
 
 
@@ -493,22 +514,17 @@ def kv_pages_fork(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_table:
     parent's full pages and gets a copy of its last, partly filled one in
     kv_pages (in place).  Returns (ref_counts, block_table, kv_lens) after the
     forks, in new tensors or in the *_out tensors, which may be the inputs."""
-    lib = load_library()
-    dev, P, R, max_pages = _tables(ref_counts, block_table, kv_lens)
+    dev, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
     layers, pages, row = _pool_shape("kv_pages", kv_pages)
-    _check(pages == P and kv_pages.device == dev, f"kv_pages must have ref_counts' {P} pages, on {dev}")
-    _ints(dev, parents=parents, children=children)
-    _check(parents.dim() == 1 and parents.shape == children.shape, "parents and children must be [n]")
-    _status_ok(status, dev)
-    n = parents.shape[0]
-    outs = (_like("ref_counts_out", ref_counts_out, ref_counts), _like("block_table_out", block_table_out, block_table),
-            _like("kv_lens_out", kv_lens_out, kv_lens))
+    if pages != P or kv_pages.device != dev:
+        raise ValueError(f"kv_pages must have ref_counts' {P} pages, on {dev}")
+    n = parents.numel()
+    forks = _vector("parents", parents, _INT32, dev, n), _vector("children", children, _INT32, dev, n)
+    outs = (_result("ref_counts_out", ref_counts_out, ref_counts), _result("block_table_out", block_table_out, block_table),
+            _result("kv_lens_out", kv_lens_out, kv_lens))
     ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R, n))
-    with _on_device(dev):
-        code = lib.kv_pages_fork(_ptr(kv_pages), P, SV_PAGE_SIZE, layers, row, _ptr(ref_counts), _ptr(block_table),
-                                 _ptr(kv_lens), R, max_pages, _ptr(parents), _ptr(children), n, *map(_ptr, outs),
-                                 _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(dev))
-    _check_status("kv_pages_fork", code)
+    _launch("kv_pages_fork", dev, kv_pages.data_ptr(), P, SV_PAGE_SIZE, layers, row, *ptrs, R, max_pages, *forks, n,
+            outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), ws.data_ptr(), ws.nbytes, _status_ptr(status, dev))
     return outs
 
 
@@ -519,19 +535,13 @@ def kv_pages_resize(ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens
     """Give request r the pages of length new_lens[r] (-1: as it is, 0: none),
     handing out the lowest free pages and taking back those behind the new
     length.  Returns (ref_counts, block_table, kv_lens) as kv_pages_fork."""
-    lib = load_library()
-    dev, P, R, max_pages = _tables(ref_counts, block_table, kv_lens)
-    _ints(dev, new_lens=new_lens)
-    _check(new_lens.shape == kv_lens.shape, "new_lens must be [R]")
-    _status_ok(status, dev)
-    outs = (_like("ref_counts_out", ref_counts_out, ref_counts), _like("block_table_out", block_table_out, block_table),
-            _like("kv_lens_out", kv_lens_out, kv_lens))
+    dev, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
+    new = _vector("new_lens", new_lens, _INT32, dev, R)
+    outs = (_result("ref_counts_out", ref_counts_out, ref_counts), _result("block_table_out", block_table_out, block_table),
+            _result("kv_lens_out", kv_lens_out, kv_lens))
     ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R))
-    with _on_device(dev):
-        code = lib.kv_pages_resize(_ptr(ref_counts), P, SV_PAGE_SIZE, _ptr(block_table), _ptr(kv_lens), R, max_pages,
-                                   _ptr(new_lens), *map(_ptr, outs), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _ptr(status), _stream(dev))
-    _check_status("kv_pages_resize", code)
+    _launch("kv_pages_resize", dev, ptrs[0], P, SV_PAGE_SIZE, ptrs[1], ptrs[2], R, max_pages, new, outs[0].data_ptr(),
+            outs[1].data_ptr(), outs[2].data_ptr(), ws.data_ptr(), ws.nbytes, _status_ptr(status, dev))
     return outs
 
 
@@ -542,37 +552,24 @@ def kv_pages_compact(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_tab
     """Move the pages in use to the front of kv_pages (in place).  Returns
     (ref_counts, block_table, page_map [P]: every page's new id or -1,
     num_live [1]); the *_out tensors may be the inputs."""
-    lib = load_library()
-    dev, P, R, max_pages = _tables(ref_counts, block_table, kv_lens)
+    dev, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
     layers, pages, row = _pool_shape("kv_pages", kv_pages)
-    _check(pages == P and kv_pages.device == dev, f"kv_pages must have ref_counts' {P} pages, on {dev}")
-    _status_ok(status, dev)
-    outs = (_like("ref_counts_out", ref_counts_out, ref_counts), _like("block_table_out", block_table_out, block_table),
-            _like("page_map", page_map, ref_counts))
+    if pages != P or kv_pages.device != dev:
+        raise ValueError(f"kv_pages must have ref_counts' {P} pages, on {dev}")
+    outs = (_result("ref_counts_out", ref_counts_out, ref_counts), _result("block_table_out", block_table_out, block_table),
+            _result("page_map", page_map, ref_counts))
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=dev)
-    _ints(dev, num_live=num_live)
-    _check(num_live.numel() == 1, "num_live must be [1]")
+        num_live = torch.empty(1, dtype=_INT32, device=dev)
+    live = _vector("num_live", num_live, _INT32, dev, 1)
     ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R))
-    with _on_device(dev):
-        code = lib.kv_pages_compact(_ptr(kv_pages), P, SV_PAGE_SIZE, layers, row, _ptr(ref_counts), _ptr(block_table),
-                                    _ptr(kv_lens), R, max_pages, *map(_ptr, outs), _ptr(num_live), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _ptr(status), _stream(dev))
-    _check_status("kv_pages_compact", code)
+    _launch("kv_pages_compact", dev, kv_pages.data_ptr(), P, SV_PAGE_SIZE, layers, row, *ptrs, R, max_pages,
+            outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), live, ws.data_ptr(), ws.nbytes,
+            _status_ptr(status, dev))
     return (*outs, num_live)
 
 
 # ------------------------------------------------------------------ sampling
 _LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
-
-
-def _setting(name: str, v, dtype: torch.dtype, T: int, dev: torch.device):
-    """(pointer, value) of a setting that is one number or a tensor [T]."""
-    if not isinstance(v, torch.Tensor):
-        return None, v
-    _check(v.dtype == dtype and v.device == dev and v.is_contiguous() and tuple(v.shape) == (T,),
-           f"{name}: a number, or {dtype}, contiguous, [T] on {dev}")
-    return v.data_ptr(), 0
 
 
 def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
@@ -583,31 +580,32 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0,
     [T] (int32 for top_k, else fp32), from uniforms [T] fp32 in [0, 1).
     Returns tokens [T] int32 or, with return_probs or a probs tensor,
     (tokens, probs [T, V] fp32): the distribution the token was drawn from."""
-    lib = load_library()
-    _check(logits.dim() == 2 and logits.dtype in _LOGITS_TYPES, "logits must be [T, V], fp32 or bf16")
+    kind = _LOGITS_TYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
+        raise ValueError("logits must be [T, V], fp32 or bf16")
     dev = logits.device
-    _check(dev.type == "cuda", "tensors must live on a CUDA device")
+    if not logits.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
     T, V = logits.shape
-    _check(V == 1 or logits.stride(1) == 1, "a row of logits must be contiguous")
-    _check(uniforms.dtype == torch.float32 and uniforms.device == dev and uniforms.is_contiguous()
-           and tuple(uniforms.shape) == (T,), f"uniforms: fp32, contiguous, [T] on {dev}")
-    settings = (*_setting("temperature", temperature, torch.float32, T, dev), *_setting("top_k", top_k, torch.int32, T, dev),
-                *_setting("top_p", top_p, torch.float32, T, dev), *_setting("min_p", min_p, torch.float32, T, dev))
+    row, col = logits.stride()
+    if col != 1 and V > 1:
+        raise ValueError("a row of logits must be contiguous")
+    if T <= 1:
+        row = V
+    elif row < V:
+        raise ValueError("rows of logits must not overlap")
+    settings = []
+    for name, v, dtype in (("temperature", temperature, _FP32), ("top_k", top_k, _INT32), ("top_p", top_p, _FP32),
+                           ("min_p", min_p, _FP32)):
+        settings += (_vector(name, v, dtype, dev, T), 0) if isinstance(v, torch.Tensor) else (None, v)
     if tokens is None:
-        tokens = torch.empty(T, dtype=torch.int32, device=dev)
-    else:
-        _ints(dev, tokens=tokens)
-        _check(tuple(tokens.shape) == (T,), "tokens must be [T]")
-    if probs is not None:
-        _check(probs.dtype == torch.float32 and probs.device == dev and probs.is_contiguous()
-               and tuple(probs.shape) == (T, V), f"probs: fp32, contiguous, [T, V] on {dev}")
-    elif return_probs:
-        probs = torch.empty((T, V), dtype=torch.float32, device=dev)
-    _status_ok(status, dev)
-    stride = logits.stride(0) if T > 1 else V
-    _check(stride >= V, "rows of logits must not overlap")
-    with _on_device(dev):
-        code = lib.sample_tokens(logits.data_ptr(), _LOGITS_TYPES[logits.dtype], T, V, stride, uniforms.data_ptr(),
-                                 *settings, tokens.data_ptr(), _ptr(probs), _ptr(status), _stream(dev))
-    _check_status("sample_tokens", code)
+        tokens = torch.empty(T, dtype=_INT32, device=dev)
+    if probs is None:
+        if return_probs:
+            probs = torch.empty((T, V), dtype=_FP32, device=dev)
+    elif probs.dtype is not _FP32 or probs.device != dev or probs.shape != logits.shape or not probs.is_contiguous():
+        raise ValueError(f"probs: fp32, contiguous, [{T}, {V}] on {dev}")
+    _launch("sample_tokens", dev, logits.data_ptr(), kind, T, V, row, _vector("uniforms", uniforms, _FP32, dev, T),
+            *settings, _vector("tokens", tokens, _INT32, dev, T), None if probs is None else probs.data_ptr(),
+            _status_ptr(status, dev))
     return tokens if probs is None else (tokens, probs)
