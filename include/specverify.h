@@ -531,8 +531,8 @@ sv_status spec_verify_sampled(const float* logits, int R, int k, int V, float te
  * the lowest index of the largest logit, probs one-hot.
  *
  * A logit of -inf (or NaN) masks its token.  A row without a finite largest
- * logit (all masked, or +inf), or with a temperature that is NaN or +inf,
- * gets token -1, probs all 0 and sets SV_DEV_BAD_LOGITS.  A uniform outside
+ * logit (all masked, or +inf), or with a temperature that is NaN or above
+ * 2^100, gets token -1, probs all 0 and sets SV_DEV_BAD_LOGITS.  A uniform outside
  * [0, 1) counts as the nearest value in it (NaN: 0), a NaN top_p or min_p as
  * off.
  *
