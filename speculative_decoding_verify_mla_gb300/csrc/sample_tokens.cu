@@ -128,23 +128,25 @@ struct SampleArgs {
 
 constexpr int kBins = 2592;       // bins of 1/64 octave of weight: 40.5 octaves, a multiple of 8 shares
 constexpr int kList = 512;        // candidates that one CTA ranks, one per thread
-constexpr int kPublished = 512;
 constexpr int kTries = 2;         // guesses of the top-p border before the bisection
+constexpr int kSlots = kWarps * kClusterMax;
+constexpr int kPublished = 512;
+constexpr int kPieces = 4;        // bulk copies of a slice
 
 struct Shared {
   uint32_t table[256];
-  u64 slot[2][3][kClusterMax];     // exchange: parity, value, rank
-  u64 warp_sum[3][kWarps];
+  __align__(16) u64 slot[2][3][kSlots];    // exchange: parity, value, (rank, warp)
   __align__(16) uint32_t pub[kPublished];  // largest keys of every warp of the cluster
-  __align__(16) u64 cand[kList];   // key << 32 | index
-  int count;                       // candidates found here
+  __align__(16) u64 cand[kList];           // candidates of this CTA: key << 32 | index
+  __align__(16) u64 list[kList];           // candidates of the cluster
+  __align__(16) u64 weight[kList];         // their weights
+  uint32_t hist[kBins];                    // see bin_estimate
+  u64 bar[kPieces];                        // arrival of the slice's pieces
+  u64 sums[2];
+  int count;                               // candidates found here
   int token;
-  uint32_t found;                  // a key, or a bin
-  int bins[2];
-  u64 before[3];                   // of the bin found: logits before and in it; at the window's start: weight
+  uint32_t found;                          // a key
   float delta[2];
-  __align__(16) u64 list[kList], sorted[kList];
-  uint32_t hist[kBins];            // see bin_estimate
 };
 
 // The weight function of a row, 2^((x - base) c).
@@ -162,13 +164,14 @@ __device__ __forceinline__ int grid256(float p, float* grid) {
   *grid = k - 49152.f;
   return (int)(__float_as_uint(k) - __float_as_uint(49152.f));
 }
-__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x) {
+__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x, int* at) {
   const float d = x - rw.base;
   const float p = d * rw.ch;
   const float e = fmaf(d, rw.cl, fmaf(d, rw.ch, -p));
   const float pc = fmaxf(p, -12000.f);  // far below every weight that counts; also -inf and NaN
   float grid;
   const int k = grid256(pc, &grid);
+  *at = k;
   const float g = (pc - grid) + e;
   // 2^g - 1
   const float r = g * fmaf(g, fmaf(g, 0.0555041087f, 0.2402265070f), 0.6931471806f);
@@ -177,6 +180,10 @@ __device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t*
   w.mant = t + (uint32_t)__float2int_rn((float)t * r);
   w.shift = min(rw.top - (k >> 8), 63);
   return w;
+}
+__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x) {
+  int at;
+  return weight_of(rw, table, x, &at);
 }
 // The lowest bit is always set: like a rounding, unlike the cut alone, that
 // is right on average, so the sum of many small weights does not drift.
@@ -203,7 +210,11 @@ __device__ __forceinline__ u64 fraction64(float f) {
 // The least integer that is the fraction f / 2^64 of v, or more.
 __device__ __forceinline__ u64 share_of(u64 f, u64 v) { return __umul64hi(f, v) + (f * v != 0 ? 1 : 0); }
 
-// Sums and maxima over the CTA and the cluster; every thread gets the result.
+// Meeting of the cluster's warps: each warp leaves its sums (or maxima) in the
+// shared memory of every CTA, then every warp adds them up for itself; one
+// cluster barrier and no CTA barrier.  Slots are in (CTA, warp) order and
+// alternate between two sets: a CTA can be one meeting ahead of a reader, not
+// two.  Lane l of a reading warp holds slots 4l .. 4l+3.
 struct Cluster {
   Shared* s;
   uint32_t rank, size;
@@ -215,78 +226,65 @@ struct Cluster {
     else
       cluster_sync();
   }
+  __device__ __forceinline__ int place() const { return (int)rank * kWarps + (int)(threadIdx.x >> 5); }
+  __device__ __forceinline__ int slots() const { return (int)size * kWarps; }
+
+  // v[i] is the same in every lane of the warp
   template <int kValues>
-  __device__ __forceinline__ void block_sum(u64 (&v)[kValues]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-      if (lane == 0) s->warp_sum[i][warp] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-      v[i] = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v[i] += s->warp_sum[i][w];
-    }
-  }
-  // Every CTA's values to every CTA; returns this exchange's slots
-  // [value][rank].  v: the same in every thread.  Slots alternate: a CTA can
-  // be one exchange ahead of a reader, not two.
-  template <int kValues>
-  __device__ __forceinline__ const u64 (*exchange(const u64 (&v)[kValues]))[kClusterMax] {
-    u64(*const to)[kClusterMax] = s->slot[parity];
+  __device__ __forceinline__ const u64 (*leave(const u64 (&v)[kValues]))[kSlots] {
+    u64(*const to)[kSlots] = s->slot[parity];
     parity ^= 1;
-    if (threadIdx.x < size) {
+    const int lane = threadIdx.x & 31;
+    if (lane < (int)size) {
 #pragma unroll
-      for (int i = 0; i < kValues; ++i) cluster_st64(cluster_map(&to[i][rank], threadIdx.x), v[i]);
+      for (int i = 0; i < kValues; ++i) cluster_st64(cluster_map(&to[i][place()], lane), v[i]);
     }
     sync();
     return to;
   }
-  template <int kValues>
-  __device__ __forceinline__ const u64 (*sum(u64 (&v)[kValues]))[kClusterMax] {
-    block_sum(v);
-    const u64(*const all)[kClusterMax] = exchange(v);
+  static __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-      v[i] = 0;
-      for (uint32_t r = 0; r < size; ++r) v[i] += all[i][r];
-    }
-    return all;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
   }
-  __device__ __forceinline__ uint32_t max(uint32_t v) {
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if ((threadIdx.x & 31) == 0) s->warp_sum[0][threadIdx.x >> 5] = v;
-    __syncthreads();
-    u64 m[1] = {0};
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) m[0] = s->warp_sum[0][w] > m[0] ? s->warp_sum[0][w] : m[0];
-    const u64(*const all)[kClusterMax] = exchange(m);
-    for (uint32_t r = 0; r < size; ++r) m[0] = all[0][r] > m[0] ? all[0][r] : m[0];
-    return (uint32_t)m[0];
-  }
-  // inclusive prefix sum over the CTA in thread order
-  __device__ __forceinline__ u64 scan(u64 v, u64* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static __device__ __forceinline__ u64 warp_scan(u64 v) {  // inclusive
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const u64 y = __shfl_up_sync(0xFFFFFFFFu, v, o);
       if (lane >= o) v += y;
     }
-    __syncthreads();
-    if (lane == 31) s->warp_sum[0][warp] = v;
-    __syncthreads();
-    u64 all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) v += s->warp_sum[0][w];
-      all += s->warp_sum[0][w];
-    }
-    *total = all;
     return v;
+  }
+  struct Four {
+    u64 v[4];
+    __device__ __forceinline__ u64 sum() const { return (v[0] + v[1]) + (v[2] + v[3]); }
+  };
+  __device__ __forceinline__ Four four(const u64* slot) const {
+    const int lane = threadIdx.x & 31;
+    Four f{};
+    if (4 * lane < slots()) {
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(slot + 4 * lane);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(slot + 4 * lane + 2);
+      f = Four{{a.x, a.y, b.x, b.y}};
+    }
+    return f;
+  }
+  // sums over the cluster of each thread's v[i]
+  template <int kValues>
+  __device__ __forceinline__ const u64 (*sum(u64 (&v)[kValues]))[kSlots] {
+#pragma unroll
+    for (int i = 0; i < kValues; ++i) v[i] = warp_sum(v[i]);
+    const u64(*const all)[kSlots] = leave(v);
+#pragma unroll
+    for (int i = 0; i < kValues; ++i) v[i] = warp_sum(four(all[i]).sum());
+    return all;
+  }
+  __device__ __forceinline__ uint32_t max(uint32_t v) {
+    const u64 w[1] = {__reduce_max_sync(0xFFFFFFFFu, v)};
+    const Four f = four(leave(w)[0]);
+    const u64 a = f.v[0] > f.v[1] ? f.v[0] : f.v[1], b = f.v[2] > f.v[3] ? f.v[2] : f.v[3];
+    return __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(a > b ? a : b));
   }
 };
 
@@ -301,31 +299,39 @@ __device__ __forceinline__ uint32_t cluster_ld(const void* p, uint32_t r) {
   return v;
 }
 
-// list[0..n) (distinct, padded with zeros to kList) in descending order into
-// out[0..n): every entry's rank is counted by a group of threads.
-__device__ __forceinline__ void sort_list(const u64* list, u64* out, int n) {
+// Threads that work on one of n items together: a power of two up to 32.
+__device__ __forceinline__ int threads_per(int n) {
   int per = 1;
   while (per < 32 && 2 * per * n <= kThreads) per *= 2;
-  const int i = (int)threadIdx.x / per, part = (int)threadIdx.x & (per - 1);
-  const u64 mine = list[i];
+  return per;
+}
+
+// For candidate i of list[0..n) (distinct, padded with zeros to kList, its
+// weight in weight[]): how many are above it, and the weight of those and its own.
+__device__ __forceinline__ int rank_of(const u64* list, const u64* weight, int n, int per, u64 mine, u64* upto) {
   int above = 0;
-  for (int j = 2 * part; j < n; j += 2 * per) {
+  u64 w = 0;
+  for (int j = 2 * ((int)threadIdx.x & (per - 1)); j < n; j += 2 * per) {
     const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j);
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(weight + j);
     above += (o.x > mine) + (o.y > mine);
+    w += (o.x >= mine ? v.x : 0) + (o.y >= mine ? v.y : 0);
   }
-  for (int o = per >> 1; o > 0; o >>= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
-  if (i < n && part == 0) out[above] = mine;
-  __syncthreads();
+  for (int o = per >> 1; o > 0; o >>= 1) {
+    above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+    w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+  }
+  *upto = w;
+  return above;
 }
 
 // The k-th largest of keys[0..n) (n a multiple of 16, k <= n) into *out.
 __device__ __forceinline__ void kth_key(const uint32_t* keys, int n, int k, uint32_t* out) {
-  int per = 1;
-  while (per < 32 && 2 * per * n <= kThreads) per *= 2;
-  const int i = (int)threadIdx.x / per, part = (int)threadIdx.x & (per - 1);
+  const int per = threads_per(n);
+  const int i = (int)threadIdx.x / per;
   const uint32_t mine = i < n ? keys[i] : 0;
   int above = 0, equal = 0;
-  for (int j = 4 * part; j < n; j += 4 * per) {
+  for (int j = 4 * ((int)threadIdx.x & (per - 1)); j < n; j += 4 * per) {
     const uint4 o = *reinterpret_cast<const uint4*>(keys + j);
     above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
     equal += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
@@ -376,22 +382,52 @@ struct Slice {
   __device__ __forceinline__ void load(int g, float (&x)[kN]) const {
     Vec<T>::unpack(kResident ? stage[g] : fetch(g), x);
   }
-  // f(x, logit of the slice) over this thread's groups: a warp owns a run of
-  // consecutive groups, its lanes neighbouring ones
-  __device__ __forceinline__ int warp_groups() const { return (groups + kWarps - 1) / kWarps; }
+  // A thread owns a run of consecutive groups (so that thread order is
+  // vocabulary order); its length is odd, which keeps the threads' 16-byte
+  // reads of shared memory in different banks.
+  __device__ __forceinline__ int run() const { return (groups + kThreads - 1) / kThreads | 1; }
+  // f(x[kN], logit of the slice of x[0]) over the thread's run ...
   template <bool kResident, class F>
-  __device__ __forceinline__ void each(F f) const {
-    const int per = warp_groups(), warp = threadIdx.x >> 5;
-    const int end = min(groups, (warp + 1) * per);
+  __device__ __forceinline__ void own(F f) const {
+    const int end = min(groups, ((int)threadIdx.x + 1) * run());
 #pragma unroll 2
-    for (int g = warp * per + (threadIdx.x & 31); g < end; g += 32) {
+    for (int g = (int)threadIdx.x * run(); g < end; ++g) {
       float x[kN];
       load<kResident>(g, x);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) f(x[i], g * kN - head + i);
+      f(x, g * kN - head);
     }
   }
+  // ... and over groups dealt out in turn, where the order does not matter
+  template <bool kResident, class F>
+  __device__ __forceinline__ void any(F f) const {
+#pragma unroll 2
+    for (int g = threadIdx.x; g < groups; g += kThreads) {
+      float x[kN];
+      load<kResident>(g, x);
+      f(x, g * kN - head);
+    }
+  }
+  // logit e of the run that starts at group g0
+  template <bool kResident>
+  __device__ __forceinline__ float at(int g0, int e) const {
+    const int i = g0 * kN - head + e;
+    if (i < 0 || i >= n) return -INFINITY;
+    if (!kResident) return Vec<T>::one(src + i);
+    const T* p = reinterpret_cast<const T*>(stage + g0) + e;
+    if constexpr (sizeof(T) == 4)
+      return *p;
+    else
+      return __bfloat162float(*p);
+  }
 };
+
+template <int kN>
+__device__ __forceinline__ float max_of(const float (&x)[kN]) {
+  float m = fmaxf(x[0], x[1]);
+#pragma unroll
+  for (int i = 2; i < kN; ++i) m = fmaxf(m, x[i]);
+  return m;
+}
 
 // m + (hi + lo) rounded up to fp32 (the sum's error by Knuth's two-sum), at
 // most m and never -inf.
@@ -402,6 +438,17 @@ __device__ __forceinline__ float add_up(float m, float hi, float lo) {
   float r = s + t;
   if (t - (r - s) > 0.f) r = nextafterf(r, INFINITY);
   return fminf(fmaxf(r, -3.402823466e38f), m);
+}
+
+// Bounded wait for a piece (it is filled once).  Where it gives up the row's
+// results mean nothing, but every CTA still takes the same path: all that
+// decides it is exchanged first.
+__device__ __forceinline__ bool wait_piece(uint32_t bar) {
+  if (mbar_test(bar, 0)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, 0))
+    if (globaltimer_ns() - t0 >= kWaitTimeoutNs) return false;
+  return true;
 }
 
 template <typename T, bool kResident>
@@ -428,21 +475,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   float min_p = a.min_p ? __ldg(a.min_p + t) : a.min_p_all;
   int top_k = a.top_k ? __ldg(a.top_k + t) : a.top_k_all;
 
-  // largest logit of the thread (fmaxf passes over NaN)
-  float m = -INFINITY;
-  {
-    const int per = sl.warp_groups(), end = min(sl.groups, (warp + 1) * per);
-#pragma unroll 4
-    for (int g = warp * per + lane; g < end; g += 32) {
-      const uint4 v = sl.fetch(g);
-      if (kResident) s_stage[g] = v;
-      float x[kN];
-      Vec<T>::unpack(v, x);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) m = fmaxf(m, x[i]);
+  // The slice comes in by bulk copies, one per piece, each with a barrier of
+  // its own, all started at once; the groups at its ends that reach beyond it
+  // are put together by threads.
+  const int inner0 = sl.head > 0 ? 1 : 0;
+  const int inner1 = sl.groups > 0 ? (sl.head + sl.n) / kN : 0;  // whole groups [inner0, inner1)
+  const int piece = (sl.groups + kPieces - 1) / kPieces;
+  if (kResident && threadIdx.x == 0) {
+    for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&s.bar[i]), 1);
+    fence_mbar_init_cluster();
+    for (int i = 0; i < kPieces; ++i) {
+      const int g0 = max(inner0, i * piece), g1 = min(inner1, (i + 1) * piece);
+      const uint32_t bar = smem_u32(&s.bar[i]);
+      if (g0 < g1) {
+        mbar_arrive_expect_tx(bar, (uint32_t)(g1 - g0) * 16u);
+        bulk_load(smem_u32(s_stage + g0), sl.src + (g0 * kN - sl.head), (uint32_t)(g1 - g0) * 16u, bar);
+      } else {
+        mbar_arrive(bar);
+      }
     }
   }
   if (threadIdx.x < 256) s.table[threadIdx.x] = kExp2.v[threadIdx.x];
+  if (kResident) {
+    if (warp == 1 && lane < 2 && sl.groups > 0) {
+      const int g = lane == 0 ? 0 : sl.groups - 1;
+      if (g < inner0 || g >= inner1) s_stage[g] = sl.fetch(g);
+    }
+    __syncthreads();
+    bool ok = true;
+    const int w0 = warp * 32 * sl.run(), w1 = w0 + 32 * sl.run();  // the warp's groups
+    for (int i = w0 / max(piece, 1); i < kPieces && i * piece < w1; ++i) ok &= wait_piece(smem_u32(&s.bar[i]));
+    if (!ok && a.status) atomicOr(a.status, SV_DEV_TIMEOUT);
+  }
+  // the thread's largest logit (fmaxf passes over NaN)
+  float top_here = -INFINITY;
+  sl.template own<kResident>([&](const float(&x)[kN], int) { top_here = fmaxf(top_here, max_of(x)); });
+
   const bool greedy = tau < 5.4210109e-20f;  // 2^-64
   if (greedy) {
     tau = 1.f;
@@ -461,34 +529,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (threadIdx.x == 0) s.count = 0;
 
   // A small top-k looks at the largest logits of every warp, at least twice as
-  // many as it asks for (measured: with fewer the candidates behind the bound
-  // grow faster than the ranking shrinks).
+  // many as it asks for: the k-th of half of them bounds about 1.4 k logits.
   int rounds = 0;
   if (top_k > 0) {
     rounds = 1;
-    while (rounds < 8 && kWarps * (int)cl.size * rounds < 2 * top_k) rounds *= 2;
-    if (kWarps * (int)cl.size * rounds < 2 * top_k || kWarps * (int)cl.size * rounds > kPublished) rounds = 0;
+    while (rounds < 8 && cl.slots() * rounds < 2 * top_k) rounds *= 2;
+    if (cl.slots() * rounds < 2 * top_k || cl.slots() * rounds > kPublished) rounds = 0;
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the cluster runs
-  float bound = -INFINITY;  // at least top_k logits reach it
+  float m, bound = -INFINITY;  // at least top_k logits reach the bound
   if (rounds > 0) {
-    uint32_t key = key_of(m);
-    const int mine = ((int)cl.rank * kWarps + warp) * rounds;
+    uint32_t key = key_of(top_here);
     for (int i = 0; i < rounds; ++i) {
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key);
-      if (lane < (int)cl.size) cluster_st(cluster_map(&s.pub[mine + i], lane), top);
+      if (lane < (int)cl.size) cluster_st(cluster_map(&s.pub[cl.place() * rounds + i], lane), top);
       const unsigned who = __ballot_sync(0xFFFFFFFFu, key == top);
       if (lane == __ffs(who) - 1) key = 0;
     }
     cl.sync();
-    const int n = kWarps * (int)cl.size * rounds;
+    const int n = cl.slots() * rounds;
     uint32_t top = 0;
     for (int i = lane; i < n; i += 32) top = max(top, s.pub[i]);
     m = key_float(__reduce_max_sync(0xFFFFFFFFu, top));
     kth_key(s.pub, n, top_k, &s.found);
     bound = key_float(s.found);
   } else {
-    m = key_float(cl.max(key_of(m)));
+    m = key_float(cl.max(key_of(top_here)));
   }
   float* const probs = a.probs ? a.probs + (long long)t * a.V + lo : nullptr;
   if (!(fabsf(m) < INFINITY) || !(tau <= kHottest)) {
@@ -523,30 +589,38 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     constexpr float kHi = (float)kWidth, kLo = (float)(kWidth - (double)kHi);
     const float hi = tau * kHi;
     base = add_up(m, -hi, -(fmaf(tau, kHi, -hi) + tau * kLo));
-    theta = min_p > 0.f ? fmaxf(base, add_up(m, s.delta[0], s.delta[1])) : base;
+    theta = base;
+    if (min_p > 0.f) theta = fmaxf(base, add_up(m, s.delta[0], s.delta[1]));
   }
   auto weight = [&](float x) { return fixed(weight_of(rw, s.table, x)); };
-  auto grid_of = [&](float x, float* off) {
-    const float p = fmaxf((x - rw.base) * rw.ch, -12000.f);
-    float grid;
-    const int k = grid256(p, &grid);
-    *off = p - grid;
-    return top_grid - k;
-  };
   auto collect = [&](float x, int i) {
     const int at = atomicAdd(&s.count, 1);
     if (at < kList) s.cand[at] = ((u64)key_of(x) << 32) | (uint32_t)(lo + i);
   };
-  // the cluster's candidates, n <= kList of them, into s.list
-  auto bring = [&](const u64* counts, int n) {
-    u64 v = 0;
-    if ((int)threadIdx.x < n) {
-      int at = (int)threadIdx.x;
-      uint32_t r = 0;
-      while (at >= (int)counts[r]) at -= (int)counts[r++];
-      v = cluster_ld64(&s.cand[at], r);
+  // The cluster's candidates, n <= kList of them, into s.list, and their
+  // weights (1 for a count) into s.weight; counts: each warp's share.
+  auto bring = [&](const u64* counts, int n, bool as_count) {
+    int of_cta = (int)cl.four(counts).sum();  // lanes 4r .. 4r+3 hold CTA r's warps
+    of_cta += __shfl_xor_sync(0xFFFFFFFFu, of_cta, 1);
+    of_cta += __shfl_xor_sync(0xFFFFFFFFu, of_cta, 2);
+    int at = (int)threadIdx.x;
+    uint32_t from = 0;
+    bool here = false;
+    for (uint32_t r = 0; r < cl.size; ++r) {
+      const int c = __shfl_sync(0xFFFFFFFFu, of_cta, 4 * r);
+      if (!here) {
+        here = at < c;
+        from = r;
+        if (!here) at -= c;
+      }
+    }
+    u64 v = 0, w = 0;
+    if (here) {
+      v = cluster_ld64(&s.cand[at], from);
+      w = as_count ? 1 : weight(key_float((uint32_t)(v >> 32)));
     }
     s.list[threadIdx.x] = v;
+    s.weight[threadIdx.x] = w;
     __syncthreads();
   };
   const u64 share = fraction64(top_p), chance = greedy ? 0 : fraction64(u);
@@ -555,45 +629,63 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   bool done = false;
   if (bound > -INFINITY) {
     // ---- small top-k: the candidates decide
-    sl.template each<kResident>([&](float x, int i) {
-      if (x >= bound) collect(x, i);
-    });
-    __syncthreads();
-    u64 mine[1] = {(u64)s.count};
-    const u64(*const counts)[kClusterMax] = cl.exchange(mine);
-    int n = 0;
-    for (uint32_t r = 0; r < cl.size; ++r) n += (int)counts[0][r];
+    u64 mine[1] = {0};
+    if (top_here >= bound)
+      sl.template own<kResident>([&](const float(&x)[kN], int i0) {
+        if (max_of(x) >= bound) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (x[i] >= bound) {
+              collect(x[i], i0 + i);
+              ++mine[0];
+            }
+        }
+      });
+    __syncwarp();
+    const u64(*const counts)[kSlots] = cl.sum(mine);
+    const int n = (int)min(mine[0], (u64)kList + 1);
     done = n <= kList;
     if (done && (probs || cl.rank == 0)) {
-      bring(counts[0], n);
-      sort_list(s.list, s.sorted, n);
-      const u64 c = (int)threadIdx.x < n ? s.sorted[threadIdx.x] : 0;
+      bring(counts[0], n, false);
+      const int per = threads_per(n), i = (int)threadIdx.x / per;
+      const bool speaks = i < n && ((int)threadIdx.x & (per - 1)) == 0;
+      const u64 c = s.list[i];  // 0 behind the last
       const float x = c ? key_float((uint32_t)(c >> 32)) : -INFINITY;
-      const float x_k = key_float((uint32_t)(s.sorted[top_k - 1] >> 32));
+      // its rank, and the weight down to it (what is outside the support has
+      // rounding dust for a weight, and comes last)
+      u64 upto;
+      const int above = rank_of(s.list, s.weight, n, per, c, &upto);
+      if (speaks && above == top_k - 1) s.found = (uint32_t)(c >> 32);
+      __syncthreads();
+      const float x_k = fmaxf(base, key_float(s.found));
       theta = fmaxf(theta, x_k);
-      const u64 w = x >= fmaxf(base, x_k) ? weight(x) : 0;
       if (top_p < 1.f) {
-        u64 all;
-        const u64 upto = cl.scan(w, &all);
-        const u64 need = max(share_of(share, all), 1ull);
-        if (upto >= need && upto - w < need) s.found = (uint32_t)(c >> 32);
+        const int in_k = __syncthreads_count(speaks && x >= x_k);
+        if (speaks && above == in_k - 1) s.sums[0] = upto;
+        __syncthreads();
+        const u64 need = max(share_of(share, s.sums[0]), 1ull);
+        if (speaks && above < in_k && upto >= need && upto - s.weight[i] < need) s.found = (uint32_t)(c >> 32);
         __syncthreads();
         theta = fmaxf(theta, key_float(s.found));
       }
-      // the kept ones, the first `kept` of the list, in the order of the vocabulary
-      const bool keep = x >= theta;
+      const bool keep = speaks && x >= theta;
       const int kept = __syncthreads_count(keep);
-      u64* const weights = reinterpret_cast<u64*>(s.hist);
-      weights[threadIdx.x] = w;
-      s.list[threadIdx.x] = keep ? ((u64)(0x7FFFFFFFu - (uint32_t)c) << 32) | threadIdx.x : 0;
+      if (keep && above == kept - 1) s.sums[1] = upto;
+      // the kept ones in the order of the vocabulary: weight up to each index
       __syncthreads();
-      sort_list(s.list, s.sorted, kept);
-      const u64 o = (int)threadIdx.x < kept ? s.sorted[threadIdx.x] : 0;
-      const u64 w_o = (int)threadIdx.x < kept ? weights[(uint32_t)o] : 0;
-      const u64 upto = cl.scan(w_o, &total);
-      const u64 target = min(__umul64hi(chance, total), total - 1);
-      if (cl.rank == 0 && upto > target && upto - w_o <= target) a.tokens[t] = (int)(0x7FFFFFFFu - (uint32_t)(o >> 32));
+      total = s.sums[1];
+      if (cl.rank == 0) {
+        const u64 target = min(__umul64hi(chance, total), total - 1);
+        u64 until = 0;
+        for (int j = (int)threadIdx.x & (per - 1); j < n; j += per) {
+          const u64 o = s.list[j];
+          if (key_float((uint32_t)(o >> 32)) >= theta && (uint32_t)o <= (uint32_t)c) until += s.weight[j];
+        }
+        for (int o = per >> 1; o > 0; o >>= 1) until += __shfl_xor_sync(0xFFFFFFFFu, until, o);
+        if (keep && until > target && until - s.weight[i] <= target) a.tokens[t] = (int)(uint32_t)c;
+      }
     }
+    if (done) cl.sync();  // nobody reads another's candidates any more
   }
   if (!done) {
     // ---- thresholds over the whole row: top-k, then top-p of what it leaves
@@ -603,202 +695,216 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       __syncthreads();
       for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist[b] = 0;
       __syncthreads();
-      sl.template each<kResident>([&](float x, int) {
-        if (x >= base) {
-          float off;
-          const int d = grid_of(x, &off);
-          const int place = ((d & 3) << 2) + min((int)(2.f - off * 1024.f), 3);
-          atomicAdd(s.hist + (d >> 2), 1u + ((uint32_t)place << kCountBits));
+      sl.template any<kResident>([&](const float(&x)[kN], int) {
+        int bin[kN];
+        uint32_t one[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          float grid;
+          const float p = fmaxf((x[i] - rw.base) * rw.ch, -12000.f);
+          const int d = top_grid - grid256(p, &grid);
+          bin[i] = d >> 2;
+          one[i] = 1u + ((uint32_t)(((d & 3) << 2) + min((int)(2.f - (p - grid) * 1024.f), 3)) << kCountBits);
         }
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (x[i] >= base) atomicAdd(s.hist + bin[i], one[i]);
       });
       cl.sync();
       // CTA r adds up share r of the bins (from the largest weights down) and
-      // leaves the sums in its own histogram, where no other CTA reads in this phase
+      // leaves the sums in its own histogram, where no other CTA reads in this
+      // phase; thread i holds `per` bins of it, so slots are in bin order too
       const int own = kBins / (int)cl.size;
       const int per = (own + kThreads - 1) / kThreads;
-      const int first = (int)threadIdx.x * per;
       constexpr int kPer = (kBins + kThreads - 1) / kThreads;
       auto edge = [&](int bin) {  // the weight at a bin's upper edge (times 2^(-1/512), as everywhere)
         const int k = top_grid - 4 * bin;
         return fixed(Weight{s.table[k & 255], min(rw.top - (k >> 8), 63)});
       };
       u64 v[2] = {0, 0};  // logits, estimated weight
-      for (int i = 0; i < per && first + i < own; ++i) {
-        const int bin = (int)cl.rank * own + first + i;
-        uint32_t c = s.hist[bin];
-        for (uint32_t r = 1; r < cl.size; ++r) c += cluster_ld(s.hist + bin, cl.rank ^ r);
-        s.hist[bin] = c;
-        v[0] += c & kCountMask;
-        v[1] += bin_estimate(c, edge(bin));
+      for (int i = 0; i < per; ++i) {
+        const int in_share = (int)threadIdx.x * per + i;
+        if (in_share < own) {
+          const int bin = (int)cl.rank * own + in_share;
+          uint32_t c = s.hist[bin];
+          for (uint32_t r = 1; r < cl.size; ++r) c += cluster_ld(s.hist + bin, cl.rank ^ r);
+          s.hist[bin] = c;
+          v[0] += c & kCountMask;
+          if (c) v[1] += bin_estimate(c, edge(bin));
+        }
       }
-      cl.block_sum(v);
-      const u64(*const shares)[kClusterMax] = cl.exchange(v);
-      u64 n_all = 0, e_all = 0, share_n[kClusterMax], share_e[kClusterMax];
-#pragma unroll
-      for (int r = 0; r < kClusterMax; ++r) {
-        share_n[r] = r < (int)cl.size ? shares[0][r] : 0;
-        share_e[r] = r < (int)cl.size ? shares[1][r] : 0;
-        n_all += share_n[r];
-        e_all += share_e[r];
-      }
+      v[0] = Cluster::warp_sum(v[0]);
+      v[1] = Cluster::warp_sum(v[1]);
+      const u64(*const shares)[kSlots] = cl.leave(v);
+      // every warp finds the border's bins by itself
+      const Cluster::Four slot_n = cl.four(shares[0]), slot_e = cl.four(shares[1]);
+      const u64 lane_n = Cluster::warp_scan(slot_n.sum()), lane_e = Cluster::warp_scan(slot_e.sum());
+      const u64 n_all = __shfl_sync(0xFFFFFFFFu, lane_n, 31), e_all = __shfl_sync(0xFFFFFFFFu, lane_e, 31);
       u64 need = (u64)top_k;
       if (!by_weight && n_all <= need) continue;  // the support holds no more
       u64 aim = by_weight ? max(share_of(share, e_all), 1ull) : need;
-      // what the bisection below searches: (low, high], `above` already there
-      float low = base, high = m;
-      u64 above = 0;
+      // what the bisection below searches: [low, high], `over` above it
+      float low = base, high = m, border = -INFINITY;
+      u64 over = 0;
       bool found = false;
-      float border = -INFINITY;
       for (int attempt = 0; attempt < kTries && !found; ++attempt) {
-        // the share, then the bin in it, where the running sum reaches the aim
-        int owner = 0;
-        u64 n_before = 0, e_before = 0;
+        // the first slot, then the first of its bins, where the running sum reaches the aim
+        u64 n0 = lane_n - slot_n.sum(), e0 = lane_e - slot_e.sum();  // before slot 4 lane + q
+        int q = -1;
 #pragma unroll
-        for (int r = 0; r + 1 < kClusterMax; ++r)
-          if (owner == r && r + 1 < (int)cl.size && (by_weight ? e_before + share_e[r] : n_before + share_n[r]) < aim) {
-            n_before += share_n[r];
-            e_before += share_e[r];
-            owner = r + 1;
+        for (int i = 0; i < 4; ++i) {
+          const u64 n1 = n0 + slot_n.v[i], e1 = e0 + slot_e.v[i];
+          if (q < 0 && (by_weight ? e1 : n1) >= aim) q = i;
+          if (q < 0) {
+            n0 = n1;
+            e0 = e1;
           }
+        }
+        unsigned who = __ballot_sync(0xFFFFFFFFu, q >= 0);
+        if (who == 0) break;  // a second guess beyond the last logit
+        const int l0 = __ffs(who) - 1;
+        const int slot = 4 * l0 + __shfl_sync(0xFFFFFFFFu, q, l0);
+        n0 = __shfl_sync(0xFFFFFFFFu, n0, l0);
+        e0 = __shfl_sync(0xFFFFFFFFu, e0, l0);
+        const int owner = slot / kWarps;
+        const int first = ((slot % kWarps) * 32 + lane) * per;
         uint32_t word[kPer];
-        u64 n_here = 0, e_here = 0, scrap;
+        u64 n_here = 0, e_here = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           word[i] = i < per && first + i < own ? cluster_ld(s.hist + owner * own + first + i, (uint32_t)owner) : 0;
           n_here += word[i] & kCountMask;
           if (by_weight && word[i]) e_here += bin_estimate(word[i], edge(owner * own + first + i));
         }
-        n_before += cl.scan(n_here, &scrap) - n_here;
-        if (by_weight) e_before += cl.scan(e_here, &scrap) - e_here;
-        if (threadIdx.x == 0) {
-          s.found = 0;
-          s.bins[0] = kBins;
-          s.bins[1] = -1;
-          s.count = 0;
-        }
-        __syncthreads();
-        // the last bin in use whose running sum before it is below the aim
-        {
-          u64 n = n_before, e = e_before;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (word[i]) {
-              if ((by_weight ? e : n) < aim) atomicMax(&s.found, (uint32_t)(owner * own + first + i) + 1);
-              n += word[i] & kCountMask;
-              if (by_weight) e += bin_estimate(word[i], edge(owner * own + first + i));
-            }
-        }
-        __syncthreads();
-        if (s.found == 0) break;  // a second guess beyond the last logit
-        const int cross = (int)s.found - 1;
-        u64 n = n_before;
+        const u64 n_first = n0 + Cluster::warp_scan(n_here) - n_here;
+        const u64 e_first = by_weight ? e0 + Cluster::warp_scan(e_here) - e_here : 0;
+        u64 n = n_first, e = e_first, cross_n = 0;
+        int cross = -1, in_cross = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          if (owner * own + first + i == cross && i < per) {
-            s.before[0] = n;
-            s.before[1] = word[i] & kCountMask;
+          const int c = (int)(word[i] & kCountMask);
+          const u64 e1 = by_weight && c ? e + bin_estimate(word[i], edge(owner * own + first + i)) : e;
+          if (cross < 0 && c && (by_weight ? e1 : n + c) >= aim) {
+            cross = owner * own + first + i;
+            cross_n = n;
+            in_cross = c;
           }
-          n += word[i] & kCountMask;
+          n += c;
+          e = e1;
         }
-        __syncthreads();
-        const u64 n_cross = s.before[0];
-        const int in_cross = (int)s.before[1];
+        who = __ballot_sync(0xFFFFFFFFu, cross >= 0);
+        if (who == 0) break;
+        const int l1 = __ffs(who) - 1;
+        cross = __shfl_sync(0xFFFFFFFFu, cross, l1);
+        cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l1);
+        in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l1);
         const bool heavy = in_cross > kList;
-        // the window: for top-p as many bins on both sides as fit the list
+        // the window: for top-p as many of these bins on both sides as fit the list
         const u64 margin = by_weight && !heavy ? (u64)(kList - in_cross) / 2 : 0;
-        n = n_before;
-        u64 e = e_before;
+        int b0 = cross, b1 = cross;
+        u64 e_b0 = ~0ull;  // the estimate before the window
+        n = n_first;
+        e = e_first;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int bin = owner * own + first + i;
+          const int c = (int)(word[i] & kCountMask);
           if (i < per && first + i < own) {
-            if (bin <= cross && n_cross - n <= margin) atomicMin(&s.bins[0], bin);
-            if (bin >= cross && n + (word[i] & kCountMask) <= n_cross + in_cross + margin) atomicMax(&s.bins[1], bin);
-          }
-          n += word[i] & kCountMask;
-        }
-        __syncthreads();
-        const int b0 = margin ? s.bins[0] : cross, b1 = margin ? s.bins[1] : cross;
-        if (by_weight) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int bin = owner * own + first + i;
-            if (bin == b0 && i < per) s.before[2] = e;
-            if (word[i]) e += bin_estimate(word[i], edge(bin));
-          }
-          __syncthreads();
-        }
-        // the exact weight above the window and of all, and what is in the window
-        u64 sums[3] = {0, 0, 0};
-        uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
-        sl.template each<kResident>([&](float x, int i) {
-          if (x >= base) {
-            float off;
-            const int b = grid_of(x, &off) >> 2;
-            if (by_weight) {
-              const u64 w = weight(x);
-              sums[1] += w;
-              if (b < b0) sums[0] += w;
+            if (bin <= cross && cross_n - n <= margin && (margin > 0 || bin == cross)) {
+              b0 = min(b0, bin);
+              e_b0 = min(e_b0, e);
             }
-            if (b >= b0 && b <= b1) {
+            if (margin > 0 && bin >= cross && n + c <= cross_n + in_cross + margin) b1 = max(b1, bin);
+          }
+          n += c;
+          if (by_weight && c) e += bin_estimate(word[i], edge(bin));
+        }
+        b0 = __reduce_min_sync(0xFFFFFFFFu, b0);
+        b1 = __reduce_max_sync(0xFFFFFFFFu, b1);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) e_b0 = min(e_b0, __shfl_xor_sync(0xFFFFFFFFu, e_b0, o));
+
+        // the exact weight above the window and of all, and what is in the window
+        if (threadIdx.x == 0) s.count = 0;
+        __syncthreads();
+        u64 sums[3] = {0, 0, 0};  // above the window, all, in the window
+        uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
+        const unsigned width = (unsigned)(b1 - b0);
+        sl.template any<kResident>([&](const float(&x)[kN], int i0) {
+          int b[kN];
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const bool in = x[i] >= base;
+            if (by_weight) {
+              int k;
+              const u64 w = in ? fixed(weight_of(rw, s.table, x[i], &k)) : 0;
+              b[i] = (top_grid - k) >> 2;
+              sums[1] += w;
+              sums[0] += b[i] < b0 ? w : 0;
+            } else {
+              float grid;
+              b[i] = (top_grid - grid256(fmaxf((x[i] - rw.base) * rw.ch, -12000.f), &grid)) >> 2;
+            }
+            if (!in) b[i] = -1;
+          }
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (b[i] >= 0 && (unsigned)(b[i] - b0) <= width) {
+              ++sums[2];
               if (heavy) {
-                key_min = min(key_min, key_of(x));
-                key_max = max(key_max, key_of(x));
+                key_min = min(key_min, key_of(x[i]));
+                key_max = max(key_max, key_of(x[i]));
               } else {
-                collect(x, i);
+                collect(x[i], i0 + i);
               }
             }
-          }
         });
         if (heavy) {
           key_max = cl.max(key_max);
-          __syncthreads();
           key_min = ~cl.max(~key_min);
-          __syncthreads();
-        } else {
-          __syncthreads();
-          if (threadIdx.x == 0) sums[2] = (u64)s.count;
         }
-        u64 mine[3] = {sums[0], sums[1], sums[2]};
-        const u64(*const all)[kClusterMax] = cl.sum(mine);
-        above = by_weight ? mine[0] : n_cross;
-        if (by_weight) need = max(share_of(share, mine[1]), 1ull);
+        const u64(*const all)[kSlots] = cl.sum(sums);
+        over = by_weight ? sums[0] : cross_n;
+        if (by_weight) need = max(share_of(share, sums[1]), 1ull);
         if (heavy) {
-          // in the bin or beside it?  (low, high] covers the bin where it is inside
-          u64 in_bin[1] = {0};
+          // is it in the bin?  [low, high] covers the bin's logits, and no others
           low = key_float(key_min);
           high = key_float(key_max);
-          sl.template each<kResident>([&](float x, int) {
-            if (x >= low && x <= high) in_bin[0] += by_weight ? weight(x) : 1;
+          u64 in_bin[1] = {0};
+          sl.template any<kResident>([&](const float(&x)[kN], int) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (x[i] >= low && x[i] <= high) in_bin[0] += by_weight ? weight(x[i]) : 1;
           });
-          __syncthreads();
           cl.sum(in_bin);
-          if (above >= need || above + in_bin[0] < need) {
+          if (over >= need || over + in_bin[0] < need) {
             low = base;
             high = m;
-            above = 0;
+            over = 0;
           }
           break;
         }
-        const int n_list = (int)mine[2];
-        bring(all[2], n_list);
-        sort_list(s.list, s.sorted, n_list);
-        const u64 c = (int)threadIdx.x < n_list ? s.sorted[threadIdx.x] : 0;
-        const u64 w = !c ? 0 : (by_weight ? weight(key_float((uint32_t)(c >> 32))) : 1);
-        u64 in_list;
-        const u64 upto = above + cl.scan(w, &in_list);
-        if (above < need && need <= above + in_list) {
-          if (upto >= need && upto - w < need) s.found = (uint32_t)(c >> 32);
-          __syncthreads();
+        const int n_list = (int)sums[2];
+        bring(all[2], n_list, !by_weight);
+        const int group = threads_per(n_list), i = (int)threadIdx.x / group;
+        const u64 c = s.list[i];
+        u64 upto;
+        rank_of(s.list, s.weight, n_list, group, c, &upto);
+        upto += over;
+        if (threadIdx.x == 0) s.found = 0;
+        __syncthreads();
+        if (c && over < need && upto >= need && upto - s.weight[i] < need) s.found = (uint32_t)(c >> 32);
+        __syncthreads();
+        if (s.found != 0) {
           border = key_float(s.found);
           found = true;
         } else {
           // the exact sums say by how much the estimate was off
-          const long long next = (long long)s.before[2] + (long long)(need - above);
+          const long long next = (long long)e_b0 + (long long)(need - over);
           aim = next < 1 ? 1 : (u64)next;
           low = base;
           high = m;
-          above = 0;
+          over = 0;
           cl.sync();  // nobody reads the candidates any more
         }
       }
@@ -809,12 +915,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const uint32_t mid = from + (to - from) / 2 + 1;
           const float vmid = key_float(mid);
           u64 c[1] = {0};
-          sl.template each<kResident>([&](float x, int) {
-            if (x >= vmid && x <= high) c[0] += by_weight ? weight(x) : 1;
+          sl.template any<kResident>([&](const float(&x)[kN], int) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (x[i] >= vmid && x[i] <= high) c[0] += by_weight ? weight(x[i]) : 1;
           });
-          __syncthreads();
           cl.sum(c);
-          if (above + c[0] >= need)
+          if (over + c[0] >= need)
             from = mid;
           else
             to = mid - 1;
@@ -827,86 +934,84 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
     // ---- the draw, in the order of the vocabulary
     u64 mine = 0;
-    sl.template each<kResident>([&](float x, int) {
-      if (x >= theta) mine += weight(x);
-    });
+    if (top_here >= theta)
+      sl.template own<kResident>([&](const float(&x)[kN], int) {
+        if (max_of(x) >= theta) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-    __syncthreads();
-    u64 sums[1] = {lane == 0 ? mine : 0};
-    const u64(*const all)[kClusterMax] = cl.sum(sums);
-    total = sums[0];
+          for (int i = 0; i < kN; ++i) mine += x[i] >= theta ? weight(x[i]) : 0;
+        }
+      });
+    __syncwarp();
+    const u64 upto = Cluster::warp_scan(mine);  // over the warp
+    const u64 of_warp[1] = {__shfl_sync(0xFFFFFFFFu, upto, 31)};
+    const Cluster::Four f = cl.four(cl.leave(of_warp)[0]);
+    const u64 until = Cluster::warp_scan(f.sum());
+    total = __shfl_sync(0xFFFFFFFFu, until, 31);
     const u64 target = min(__umul64hi(chance, total), total - 1);
-    u64 before = 0;
-    for (uint32_t r = 0; r < cl.rank; ++r) before += all[0][r];
-    for (int w = 0; w < warp; ++w) before += s.warp_sum[0][w];
-    if (target >= before && target - before < mine) {
-      // this warp holds the token
-      const int per = sl.warp_groups(), end = min(sl.groups, (warp + 1) * per);
-      u64 run = before;
-      for (int g0 = warp * per; g0 < end; g0 += 32) {
-        const int g = g0 + lane;
-        float x[kN];
-        u64 w[kN], sum = 0;
-        if (g < end) {
-          sl.template load<kResident>(g, x);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kN; ++i) x[i] = -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          w[i] = x[i] >= theta ? weight(x[i]) : 0;
-          sum += w[i];
-        }
-        u64 incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const u64 upto = run + incl - sum;
-        if (target >= upto && target < upto + sum) {
-          u64 c = upto;
-          int hit = -1;
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            c += w[i];
-            if (hit < 0 && c > target) hit = i;
-          }
-          const int token = (int)(lo + g * kN - sl.head + hit);
+    // the weight before this warp: slot `place`
+    const int sub = cl.place() & 3;
+    const u64 mine4 = until - f.sum() + (sub > 0 ? f.v[0] : 0) + (sub > 1 ? f.v[1] : 0) + (sub > 2 ? f.v[2] : 0);
+    const u64 before = __shfl_sync(0xFFFFFFFFu, mine4, cl.place() >> 2);
+    if (target >= before && target - before < of_warp[0]) {
+      // this warp holds the token: its lane, then the lane's logits side by side
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, before + upto > target);
+      const int l0 = __ffs(who) - 1;
+      u64 run = before + __shfl_sync(0xFFFFFFFFu, upto - mine, l0);
+      const int g0 = (warp * 32 + l0) * sl.run(), n = sl.run() * kN;
+      for (int e0 = 0; e0 < n; e0 += 32) {
+        const int e = e0 + lane;
+        const float x = e < n ? sl.template at<kResident>(g0, e) : -INFINITY;
+        const u64 w = x >= theta ? weight(x) : 0;
+        const u64 incl = run + Cluster::warp_scan(w);
+        if (w != 0 && incl > target && incl - w <= target) {
+          const int token = (int)(lo + g0 * kN - sl.head + e);
           a.tokens[t] = token;
           if (probs && greedy)
             for (uint32_t r = 0; r < cl.size; ++r) cluster_st(cluster_map(&s.token, r), (uint32_t)token);
         }
-        run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        run = __shfl_sync(0xFFFFFFFFu, incl, 31);
         if (run > target) break;
       }
     }
   }
-  cl.sync();  // the token is known; no CTA reads another's shared memory any more
   if (!probs) return;
   if (greedy) {
+    cl.sync();  // the token is known
     for (int i = threadIdx.x; i < sl.n; i += kThreads) probs[i] = lo + i == s.token ? 1.f : 0.f;
     return;
   }
   if (threadIdx.x == 0) s.delta[0] = (float)(1.0 / (double)total);
   __syncthreads();
   const float inv = s.delta[0];
-  sl.template each<kResident>([&](float x, int i) {
-    if (i < 0 || i >= sl.n) return;
-    float p = 0.f;
-    if (x >= theta) {
-      const Weight w = weight_of(rw, s.table, x);
-      p = (float)w.mant * __uint_as_float((uint32_t)(127 + 31 - w.shift) << 23) * inv;
+  const bool wide = ((reinterpret_cast<uintptr_t>(probs) - 4u * sl.head) & 15u) == 0;  // groups at 16-byte addresses
+  sl.template any<kResident>([&](const float(&x)[kN], int i0) {
+    float p[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) p[i] = 0.f;
+    if (max_of(x) >= theta) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (x[i] >= theta) {
+          const Weight w = weight_of(rw, s.table, x[i]);
+          p[i] = (float)w.mant * __uint_as_float((uint32_t)(127 + 31 - w.shift) << 23) * inv;
+        }
     }
-    probs[i] = p;
+    if (wide && i0 >= 0 && i0 + kN <= sl.n) {
+#pragma unroll
+      for (int i = 0; i < kN; i += 4)
+        __stcs(reinterpret_cast<float4*>(probs + i0 + i), make_float4(p[i], p[i + 1], p[i + 2], p[i + 3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (i0 + i >= 0 && i0 + i < sl.n) probs[i0 + i] = p[i];
+    }
   });
 }
 
 // ------------------------------------------------------------------ host side
-constexpr size_t kStageTwo = 86 * 1024;   // two CTAs of an SM keep their slices
-constexpr size_t kStageOne = 196 * 1024;  // one CTA does
+// 228 KB of an SM, 1 KB of it taken per CTA; at most 227 KB for one
+constexpr size_t kStageTwo = (114 * 1024 - 1024 - sizeof(Shared) - 64) / 16 * 16;   // two CTAs of an SM keep their slices
+constexpr size_t kStageOne = (227 * 1024 - sizeof(Shared) - 64) / 16 * 16;          // one CTA does
 
 struct Shape {
   int ctas, slice;
