@@ -18,9 +18,9 @@
 // are 64-bit integers: they are associative, and the token is a function of
 // the inputs alone.  The weight is
 // 2^t with t = x * log2(e)/temperature carried as an unevaluated fp32 pair,
-// split as t = k/256 + g with integer k; 2^(k/256) comes from a table of 256
-// integers and 2^g - 1, |g| <= 1/512, from three Taylor terms (the table
-// method of Tang 1989).
+// split as t = k/512 + g with integer k; 2^(k/512) comes from a table of 512
+// integers and 2^g - 1, |g| <= 1/1024, from two Taylor terms (the table
+// method of Tang 1989; the third term is below 2^-34).
 //
 // One thread-block cluster per row; each CTA keeps its slice of the row in
 // shared memory, so the logits cross HBM once whatever the filters need, and
@@ -52,18 +52,20 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+static_assert(kThreads == 512, "a thread per table entry and per candidate");
 constexpr int kClusterMax = 8;
 constexpr int kSupportBits = 40;     // weights below 2^-40 of the largest are left out
 constexpr int kMaxVocab = 1 << 22;   // leaves a weight 41 bits
 constexpr float kHottest = 1.2676506e30f;  // 2^100: beyond, 1/temperature loses bits
-constexpr float kCoarseMax = 8192.f;  // |x| log2(e)/temperature up to which the row needs no shift
+constexpr float kCoarseMax = 4096.f;  // |x| log2(e)/temperature up to which the row needs no shift
 
-// round(2^31 2^(j/256)), j = 0..255, by the exponential series.
+// round(2^31 2^(j/512)), j = 0..511, by the exponential series.
+constexpr int kGrid = 512, kGridBits = 9;
 struct Exp2Table {
-  uint32_t v[256];
+  uint32_t v[kGrid];
   constexpr Exp2Table() : v() {
-    for (int j = 0; j < 256; ++j) {
-      const double y = j * 0.693147180559945309417232121458 / 256.0;
+    for (int j = 0; j < kGrid; ++j) {
+      const double y = j * 0.693147180559945309417232121458 / kGrid;
       double term = 1.0, sum = 1.0;
       for (int i = 1; i < 24; ++i) {
         term *= y / i;
@@ -128,13 +130,14 @@ struct SampleArgs {
 
 constexpr int kBins = 2592;       // bins of 1/64 octave of weight: 40.5 octaves, a multiple of 8 shares
 constexpr int kList = 512;        // candidates that one CTA ranks, one per thread
+constexpr int kMargin = 64;       // logits on both sides of the bin in which top-p's border is expected
 constexpr int kTries = 2;         // guesses of the top-p border before the bisection
 constexpr int kSlots = kWarps * kClusterMax;
 constexpr int kPublished = 512;
 constexpr int kPieces = 4;        // bulk copies of a slice
 
 struct Shared {
-  uint32_t table[256];
+  uint32_t table[kGrid];
   __align__(16) u64 slot[2][3][kSlots];    // exchange: parity, value, (rank, warp)
   __align__(16) uint32_t pub[kPublished];  // largest keys of every warp of the cluster
   __align__(16) u64 cand[kList];           // candidates of this CTA: key << 32 | index
@@ -158,27 +161,30 @@ struct Weight {
   uint32_t mant;  // [2^31, 2^32)
   int shift;      // the weight is (mant << 31) >> shift
 };
-__device__ __forceinline__ int grid256(float p, float* grid) {
-  // p rounded to a multiple of 1/256: adding 1.5 * 2^15 leaves 8 fraction bits
-  const float k = p + 49152.f;
-  *grid = k - 49152.f;
-  return (int)(__float_as_uint(k) - __float_as_uint(49152.f));
+__device__ __forceinline__ int grid_of(float p, float* grid) {
+  // p rounded to a multiple of 1/512: adding 1.5 * 2^14 leaves 9 fraction bits
+  const float k = p + 24576.f;
+  *grid = k - 24576.f;
+  return (int)(__float_as_uint(k) - __float_as_uint(24576.f));
 }
+constexpr float kLowest = -7000.f;  // in place of every t far below those that count, -inf and NaN
 __device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x, int* at) {
   const float d = x - rw.base;
   const float p = d * rw.ch;
   const float e = fmaf(d, rw.cl, fmaf(d, rw.ch, -p));
-  const float pc = fmaxf(p, -12000.f);  // far below every weight that counts; also -inf and NaN
+  const float pc = fmaxf(p, kLowest);
   float grid;
-  const int k = grid256(pc, &grid);
+  const int k = grid_of(pc, &grid);
   *at = k;
   const float g = (pc - grid) + e;
-  // 2^g - 1
-  const float r = g * fmaf(g, fmaf(g, 0.0555041087f, 0.2402265070f), 0.6931471806f);
+  const float r = g * fmaf(g, 0.2402265070f, 0.6931471806f);  // 2^g - 1
   Weight w;
-  const uint32_t t = table[k & 255];
-  w.mant = t + (uint32_t)__float2int_rn((float)t * r);
-  w.shift = min(rw.top - (k >> 8), 63);
+  const uint32_t t = table[k & (kGrid - 1)];
+  // t r, rounded to an integer by adding 1.5 * 2^23 (|t r| < 2^22); t as fp32
+  // by its bits: 2^31 <= t < 2^32
+  const float tf = __uint_as_float((t >> 8) + 0x4E800000u);
+  w.mant = t + (__float_as_uint(fmaf(tf, r, 12582912.f)) - 0x4B400000u);
+  w.shift = min(rw.top - (k >> kGridBits), 63);
   return w;
 }
 __device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x) {
@@ -299,6 +305,17 @@ __device__ __forceinline__ uint32_t cluster_ld(const void* p, uint32_t r) {
   return v;
 }
 
+template <typename V>
+__device__ __forceinline__ V scan_add(V v) {  // inclusive, over the warp
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
 // Threads that work on one of n items together: a power of two up to 32.
 __device__ __forceinline__ int threads_per(int n) {
   int per = 1;
@@ -348,12 +365,15 @@ __device__ __forceinline__ void kth_key(const uint32_t* keys, int n, int k, uint
 // of their places 0..15 in the bin, which is right for up to 32 of them.
 constexpr int kCountBits = 23;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
-// (2 places + 1) / 32 of a bin below its edge: a share of 2^(1/64) - 1 of 88/2^13 per bin
-__device__ __forceinline__ u64 bin_estimate(uint32_t word, u64 edge) {
-  const u64 c = word & kCountMask;
-  const u64 places = c <= 32 ? word >> kCountBits : (15 * c) / 2;
-  return c * edge - (edge >> 18) * (2 * places + c) * 88;
+// Estimated weight of a bin, in units of the weight of the largest logit's
+// grid point: within a bin the weight falls by 1 - 2^(-1/64) = 0.010772.
+__device__ __forceinline__ float bin_estimate(uint32_t word, int bin) {
+  const float c = (float)(word & kCountMask);
+  const float places = c <= 32.f ? (float)(word >> kCountBits) : 7.5f * c;
+  return fast_exp2((float)bin * -0.015625f) * (c - (2.f * places + c) * (0.010772f / 32.f));
 }
+// (logits, estimate) as one word of an exchange
+__device__ __forceinline__ u64 pack_est(uint32_t n, float e) { return ((u64)n << 32) | __float_as_uint(e); }
 
 // The CTA's slice of the row as groups of 16 aligned bytes; element i of group
 // g is logit g * kN - head + i of the slice, -inf where that is outside it.
@@ -495,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
   }
-  if (threadIdx.x < 256) s.table[threadIdx.x] = kExp2.v[threadIdx.x];
+  s.table[threadIdx.x] = kExp2.v[threadIdx.x];
   if (kResident) {
     if (warp == 1 && lane < 2 && sl.groups > 0) {
       const int g = lane == 0 ? 0 : sl.groups - 1;
@@ -579,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     rw.cl = (fmaf(-rw.ch, tau, 1.44269502f) + 1.92596299e-8f) / tau;
     rw.base = fabsf(m * rw.ch) < kCoarseMax ? 0.f : m;
     float grid;
-    top_grid = grid256((m - rw.base) * rw.ch, &grid);
-    rw.top = (top_grid >> 8) + a.down;
+    top_grid = grid_of((m - rw.base) * rw.ch, &grid);
+    rw.top = (top_grid >> kGridBits) + a.down;
   }
   // the support ends 40 ln 2 temperatures below m
   float base, theta;
@@ -695,16 +715,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       __syncthreads();
       for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist[b] = 0;
       __syncthreads();
+      // the histogram and, for top-p, the exact weight of all
+      u64 all[1] = {0};
       sl.template any<kResident>([&](const float(&x)[kN], int) {
         int bin[kN];
         uint32_t one[kN];
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
+          const float p = fmaxf((x[i] - rw.base) * rw.ch, kLowest);
           float grid;
-          const float p = fmaxf((x[i] - rw.base) * rw.ch, -12000.f);
-          const int d = top_grid - grid256(p, &grid);
-          bin[i] = d >> 2;
-          one[i] = 1u + ((uint32_t)(((d & 3) << 2) + min((int)(2.f - (p - grid) * 1024.f), 3)) << kCountBits);
+          int k = grid_of(p, &grid);
+          if (by_weight) {
+            const u64 w = fixed(weight_of(rw, s.table, x[i], &k));
+            all[0] += x[i] >= base ? w : 0;
+          }
+          const int d = top_grid - k;
+          bin[i] = d >> 3;
+          one[i] = 1u + ((uint32_t)(((d & 7) << 1) + (p < grid ? 1 : 0)) << kCountBits);
         }
 #pragma unroll
         for (int i = 0; i < kN; ++i)
@@ -717,140 +744,191 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       const int own = kBins / (int)cl.size;
       const int per = (own + kThreads - 1) / kThreads;
       constexpr int kPer = (kBins + kThreads - 1) / kThreads;
-      auto edge = [&](int bin) {  // the weight at a bin's upper edge (times 2^(-1/512), as everywhere)
-        const int k = top_grid - 4 * bin;
-        return fixed(Weight{s.table[k & 255], min(rw.top - (k >> 8), 63)});
-      };
-      u64 v[2] = {0, 0};  // logits, estimated weight
-      for (int i = 0; i < per; ++i) {
-        const int in_share = (int)threadIdx.x * per + i;
-        if (in_share < own) {
-          const int bin = (int)cl.rank * own + in_share;
-          uint32_t c = s.hist[bin];
-          for (uint32_t r = 1; r < cl.size; ++r) c += cluster_ld(s.hist + bin, cl.rank ^ r);
-          s.hist[bin] = c;
-          v[0] += c & kCountMask;
-          if (c) v[1] += bin_estimate(c, edge(bin));
+      u64 v[2] = {0, Cluster::warp_sum(all[0])};
+      {
+        uint32_t n = 0;
+        float e = 0.f;
+        for (int i = 0; i < per; ++i) {
+          const int in_share = (int)threadIdx.x * per + i;
+          if (in_share < own) {
+            const int bin = (int)cl.rank * own + in_share;
+            uint32_t c[kClusterMax];
+#pragma unroll
+            for (uint32_t r = 1; r < kClusterMax; ++r) c[r] = r < cl.size ? cluster_ld(s.hist + bin, cl.rank ^ r) : 0;
+            c[0] = s.hist[bin];
+#pragma unroll
+            for (uint32_t r = 1; r < kClusterMax; ++r) c[0] += c[r];
+            s.hist[bin] = c[0];
+            n += c[0] & kCountMask;
+            e += bin_estimate(c[0], bin);
+          }
         }
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
+        v[0] = pack_est(n, e);
       }
-      v[0] = Cluster::warp_sum(v[0]);
-      v[1] = Cluster::warp_sum(v[1]);
       const u64(*const shares)[kSlots] = cl.leave(v);
       // every warp finds the border's bins by itself
-      const Cluster::Four slot_n = cl.four(shares[0]), slot_e = cl.four(shares[1]);
-      const u64 lane_n = Cluster::warp_scan(slot_n.sum()), lane_e = Cluster::warp_scan(slot_e.sum());
-      const u64 n_all = __shfl_sync(0xFFFFFFFFu, lane_n, 31), e_all = __shfl_sync(0xFFFFFFFFu, lane_e, 31);
+      const Cluster::Four slot = cl.four(shares[0]);
+      uint32_t slot_n[4], lane_n = 0;
+      float slot_e[4], lane_e = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lane_n += slot_n[i] = (uint32_t)(slot.v[i] >> 32);
+        lane_e += slot_e[i] = __uint_as_float((uint32_t)slot.v[i]);
+      }
+      lane_n = scan_add(lane_n);
+      lane_e = scan_add(lane_e);
+      const uint32_t n_all = __shfl_sync(0xFFFFFFFFu, lane_n, 31);
+      const float e_all = __shfl_sync(0xFFFFFFFFu, lane_e, 31);
       u64 need = (u64)top_k;
-      if (!by_weight && n_all <= need) continue;  // the support holds no more
-      u64 aim = by_weight ? max(share_of(share, e_all), 1ull) : need;
+      if (by_weight)
+        need = max(share_of(share, Cluster::warp_sum(cl.four(shares[1]).sum())), 1ull);
+      else if (n_all <= (uint32_t)top_k)
+        continue;  // the support holds no more
+      // the border is where the running sum reaches the aim: exact for counts
+      float aim = by_weight ? fmaxf(top_p, 0.f) * e_all : 0.f;
       // what the bisection below searches: [low, high], `over` above it
       float low = base, high = m, border = -INFINITY;
       u64 over = 0;
       bool found = false;
       for (int attempt = 0; attempt < kTries && !found; ++attempt) {
         // the first slot, then the first of its bins, where the running sum reaches the aim
-        u64 n0 = lane_n - slot_n.sum(), e0 = lane_e - slot_e.sum();  // before slot 4 lane + q
+        const uint32_t up_n = __shfl_up_sync(0xFFFFFFFFu, lane_n, 1);
+        const float up_e = __shfl_up_sync(0xFFFFFFFFu, lane_e, 1);
+        uint32_t n = lane > 0 ? up_n : 0;  // before slot 4 lane + q
+        float e = lane > 0 ? up_e : 0.f;
         int q = -1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const u64 n1 = n0 + slot_n.v[i], e1 = e0 + slot_e.v[i];
-          if (q < 0 && (by_weight ? e1 : n1) >= aim) q = i;
+        for (int i = 0; i < 4; ++i)
           if (q < 0) {
-            n0 = n1;
-            e0 = e1;
+            if (slot_n[i] > 0 && (by_weight ? e + slot_e[i] >= aim : n + slot_n[i] >= (uint32_t)top_k)) {
+              q = i;
+            } else {
+              n += slot_n[i];
+              e += slot_e[i];
+            }
           }
-        }
         unsigned who = __ballot_sync(0xFFFFFFFFu, q >= 0);
-        if (who == 0) break;  // a second guess beyond the last logit
-        const int l0 = __ffs(who) - 1;
-        const int slot = 4 * l0 + __shfl_sync(0xFFFFFFFFu, q, l0);
-        n0 = __shfl_sync(0xFFFFFFFFu, n0, l0);
-        e0 = __shfl_sync(0xFFFFFFFFu, e0, l0);
-        const int owner = slot / kWarps;
-        const int first = ((slot % kWarps) * 32 + lane) * per;
-        uint32_t word[kPer];
-        u64 n_here = 0, e_here = 0;
+        if (who == 0) break;  // (rounding, or a second guess) beyond the last logit
+        int l0 = __ffs(who) - 1;
+        const int at = 4 * l0 + __shfl_sync(0xFFFFFFFFu, q, l0);
+        n = __shfl_sync(0xFFFFFFFFu, n, l0);
+        e = __shfl_sync(0xFFFFFFFFu, e, l0);
+        const int owner = at / kWarps;
+        const int first = ((at % kWarps) * 32 + lane) * per;
+        uint32_t word[kPer], n_here = 0;
+        float est[kPer], e_here = 0.f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           word[i] = i < per && first + i < own ? cluster_ld(s.hist + owner * own + first + i, (uint32_t)owner) : 0;
+          est[i] = bin_estimate(word[i], owner * own + first + i);
           n_here += word[i] & kCountMask;
-          if (by_weight && word[i]) e_here += bin_estimate(word[i], edge(owner * own + first + i));
+          e_here += est[i];
         }
-        const u64 n_first = n0 + Cluster::warp_scan(n_here) - n_here;
-        const u64 e_first = by_weight ? e0 + Cluster::warp_scan(e_here) - e_here : 0;
-        u64 n = n_first, e = e_first, cross_n = 0;
+        n += scan_add(n_here) - n_here;
+        e += scan_add(e_here) - e_here;
+        const uint32_t n_first = n;
+        const float e_first = e;
         int cross = -1, in_cross = 0;
+        uint32_t cross_n = 0;
+        float cross_e = 0.f;
+        int last = -1;  // if rounding keeps all of them below the aim: the last one in use
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int c = (int)(word[i] & kCountMask);
-          const u64 e1 = by_weight && c ? e + bin_estimate(word[i], edge(owner * own + first + i)) : e;
-          if (cross < 0 && c && (by_weight ? e1 : n + c) >= aim) {
+          const uint32_t c = word[i] & kCountMask;
+          if (c) last = i;
+          if (cross < 0 && c && (by_weight ? e + est[i] >= aim : n + c >= (uint32_t)top_k)) {
             cross = owner * own + first + i;
             cross_n = n;
-            in_cross = c;
+            cross_e = e;
+            in_cross = (int)c;
           }
           n += c;
-          e = e1;
+          e += est[i];
         }
         who = __ballot_sync(0xFFFFFFFFu, cross >= 0);
-        if (who == 0) break;
-        const int l1 = __ffs(who) - 1;
-        cross = __shfl_sync(0xFFFFFFFFu, cross, l1);
-        cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l1);
-        in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l1);
+        if (who == 0) {
+          n = n_first;
+          e = e_first;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            if (i == last) {
+              cross = owner * own + first + i;
+              cross_n = n;
+              cross_e = e;
+              in_cross = (int)(word[i] & kCountMask);
+            }
+            n += word[i] & kCountMask;
+            e += est[i];
+          }
+          who = __ballot_sync(0xFFFFFFFFu, last >= 0);
+          l0 = 31 - __clz(who);
+        } else {
+          l0 = __ffs(who) - 1;
+        }
+        cross = __shfl_sync(0xFFFFFFFFu, cross, l0);
+        cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l0);
+        cross_e = __shfl_sync(0xFFFFFFFFu, cross_e, l0);
+        in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l0);
         const bool heavy = in_cross > kList;
-        // the window: for top-p as many of these bins on both sides as fit the list
-        const u64 margin = by_weight && !heavy ? (u64)(kList - in_cross) / 2 : 0;
+        // the window: for top-p some logits of the bins on both sides
+        const uint32_t margin = by_weight && !heavy ? (uint32_t)min(kMargin, (kList - in_cross) / 2) : 0;
         int b0 = cross, b1 = cross;
-        u64 e_b0 = ~0ull;  // the estimate before the window
+        float e_b0 = cross_e;  // the estimate before the window
         n = n_first;
         e = e_first;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int bin = owner * own + first + i;
-          const int c = (int)(word[i] & kCountMask);
-          if (i < per && first + i < own) {
-            if (bin <= cross && cross_n - n <= margin && (margin > 0 || bin == cross)) {
+          const uint32_t c = word[i] & kCountMask;
+          if (margin > 0 && i < per && first + i < own) {
+            if (bin < cross && cross_n - n <= margin) {
               b0 = min(b0, bin);
-              e_b0 = min(e_b0, e);
+              e_b0 = fminf(e_b0, e);
             }
-            if (margin > 0 && bin >= cross && n + c <= cross_n + in_cross + margin) b1 = max(b1, bin);
+            if (bin > cross && n + c <= cross_n + in_cross + margin) b1 = max(b1, bin);
           }
           n += c;
-          if (by_weight && c) e += bin_estimate(word[i], edge(bin));
+          e += est[i];
         }
         b0 = __reduce_min_sync(0xFFFFFFFFu, b0);
         b1 = __reduce_max_sync(0xFFFFFFFFu, b1);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) e_b0 = min(e_b0, __shfl_xor_sync(0xFFFFFFFFu, e_b0, o));
+        for (int o = 16; o > 0; o >>= 1) e_b0 = fminf(e_b0, __shfl_xor_sync(0xFFFFFFFFu, e_b0, o));
+        // Every logit of the bins up to b1 is above `floor`: the bin's lower
+        // edge, two grid steps and the rounding of |t| < 2^13 further down.
+        const float floor_t = (float)(top_grid - 8 * (b1 + 1) - 2) * (1.f / kGrid);
+        const float floor = (floor_t - fabsf(floor_t) * 0x1p-20f) / rw.ch;
+        const float edge = fmaxf(base, (floor - fabsf(floor) * 0x1p-20f) + (rw.base - fabsf(rw.base) * 0x1p-22f));
 
-        // the exact weight above the window and of all, and what is in the window
+        // the exact weight above the window, and what is in the window
         if (threadIdx.x == 0) s.count = 0;
         __syncthreads();
-        u64 sums[3] = {0, 0, 0};  // above the window, all, in the window
+        u64 sums[2] = {0, 0};  // above the window, logits in it
         uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
         const unsigned width = (unsigned)(b1 - b0);
         sl.template any<kResident>([&](const float(&x)[kN], int i0) {
+          if (!(max_of(x) >= edge)) return;
           int b[kN];
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
-            const bool in = x[i] >= base;
+            int k;
             if (by_weight) {
-              int k;
-              const u64 w = in ? fixed(weight_of(rw, s.table, x[i], &k)) : 0;
-              b[i] = (top_grid - k) >> 2;
-              sums[1] += w;
-              sums[0] += b[i] < b0 ? w : 0;
+              const u64 w = fixed(weight_of(rw, s.table, x[i], &k));
+              b[i] = (top_grid - k) >> 3;
+              sums[0] += b[i] < b0 && x[i] >= base ? w : 0;
             } else {
               float grid;
-              b[i] = (top_grid - grid256(fmaxf((x[i] - rw.base) * rw.ch, -12000.f), &grid)) >> 2;
+              b[i] = (top_grid - grid_of(fmaxf((x[i] - rw.base) * rw.ch, kLowest), &grid)) >> 3;
             }
-            if (!in) b[i] = -1;
+            if (!(x[i] >= base)) b[i] = -1;
           }
 #pragma unroll
           for (int i = 0; i < kN; ++i)
             if (b[i] >= 0 && (unsigned)(b[i] - b0) <= width) {
-              ++sums[2];
+              ++sums[1];
               if (heavy) {
                 key_min = min(key_min, key_of(x[i]));
                 key_max = max(key_max, key_of(x[i]));
@@ -859,13 +937,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
               }
             }
         });
+        __syncwarp();
         if (heavy) {
           key_max = cl.max(key_max);
           key_min = ~cl.max(~key_min);
         }
-        const u64(*const all)[kSlots] = cl.sum(sums);
+        const u64(*const met)[kSlots] = cl.sum(sums);
         over = by_weight ? sums[0] : cross_n;
-        if (by_weight) need = max(share_of(share, sums[1]), 1ull);
         if (heavy) {
           // is it in the bin?  [low, high] covers the bin's logits, and no others
           low = key_float(key_min);
@@ -876,6 +954,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             for (int i = 0; i < kN; ++i)
               if (x[i] >= low && x[i] <= high) in_bin[0] += by_weight ? weight(x[i]) : 1;
           });
+          __syncwarp();
           cl.sum(in_bin);
           if (over >= need || over + in_bin[0] < need) {
             low = base;
@@ -884,8 +963,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           }
           break;
         }
-        const int n_list = (int)sums[2];
-        bring(all[2], n_list, !by_weight);
+        const int n_list = (int)sums[1];
+        bring(met[1], n_list, !by_weight);
         const int group = threads_per(n_list), i = (int)threadIdx.x / group;
         const u64 c = s.list[i];
         u64 upto;
@@ -900,8 +979,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           found = true;
         } else {
           // the exact sums say by how much the estimate was off
-          const long long next = (long long)e_b0 + (long long)(need - over);
-          aim = next < 1 ? 1 : (u64)next;
+          const float unit = (float)fixed(Weight{s.table[top_grid & (kGrid - 1)], rw.top - (top_grid >> kGridBits)});
+          aim = fmaxf(e_b0 + (float)(long long)(need - over) / unit, 0.f);
           low = base;
           high = m;
           over = 0;
@@ -920,6 +999,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             for (int i = 0; i < kN; ++i)
               if (x[i] >= vmid && x[i] <= high) c[0] += by_weight ? weight(x[i]) : 1;
           });
+          __syncwarp();
           cl.sum(c);
           if (over + c[0] >= need)
             from = mid;
@@ -938,7 +1018,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sl.template own<kResident>([&](const float(&x)[kN], int) {
         if (max_of(x) >= theta) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) mine += x[i] >= theta ? weight(x[i]) : 0;
+          for (int i = 0; i < kN; ++i) {
+            const u64 w = weight(x[i]);
+            mine += x[i] >= theta ? w : 0;
+          }
         }
       });
     __syncwarp();
