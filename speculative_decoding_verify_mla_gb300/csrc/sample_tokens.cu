@@ -135,6 +135,7 @@ constexpr int kTries = 2;         // guesses of the top-p border before the bise
 constexpr int kSlots = kWarps * kClusterMax;
 constexpr int kPublished = 512;
 constexpr int kPieces = 4;        // bulk copies of a slice
+constexpr int kHold = 4;          // groups a thread holds when the token is looked up
 
 struct Shared {
   uint32_t table[kGrid];
@@ -251,15 +252,6 @@ struct Cluster {
   static __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-  }
-  static __device__ __forceinline__ u64 warp_scan(u64 v) {  // inclusive
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 y = __shfl_up_sync(0xFFFFFFFFu, v, o);
-      if (lane >= o) v += y;
-    }
     return v;
   }
   struct Four {
@@ -398,46 +390,32 @@ struct Slice {
     for (int i = 0; i < kN; ++i) x[i] = e0 + i >= 0 && e0 + i < n ? Vec<T>::one(src + e0 + i) : -INFINITY;
     return Vec<T>::pack(x);
   }
-  template <bool kResident>
-  __device__ __forceinline__ void load(int g, float (&x)[kN]) const {
-    Vec<T>::unpack(kResident ? stage[g] : fetch(g), x);
+  static __device__ __forceinline__ uint4 nothing() {  // a group of -inf
+    constexpr uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+    return make_uint4(w, w, w, w);
   }
-  // A thread owns a run of consecutive groups (so that thread order is
-  // vocabulary order); its length is odd, which keeps the threads' 16-byte
-  // reads of shared memory in different banks.
-  __device__ __forceinline__ int run() const { return (groups + kThreads - 1) / kThreads | 1; }
-  // f(x[kN], logit of the slice of x[0]) over the thread's run ...
-  template <bool kResident, class F>
+  template <bool kResident>
+  __device__ __forceinline__ uint4 raw(int g) const {
+    return kResident ? stage[g] : fetch(g);
+  }
+  // A warp owns a run of consecutive groups, dealt out to its lanes in turn.
+  __device__ __forceinline__ int run() const { return (groups + kWarps - 1) / kWarps; }
+  // f(x[kN], logit of the slice of x[0], group) over the thread's groups, kBatch loads at a time
+  template <bool kResident, int kBatch, class F>
   __device__ __forceinline__ void own(F f) const {
-    const int end = min(groups, ((int)threadIdx.x + 1) * run());
-#pragma unroll 2
-    for (int g = (int)threadIdx.x * run(); g < end; ++g) {
-      float x[kN];
-      load<kResident>(g, x);
-      f(x, g * kN - head);
+    const int w = (int)threadIdx.x >> 5, end = min(groups, (w + 1) * run());
+    for (int g0 = w * run() + ((int)threadIdx.x & 31); g0 < end; g0 += 32 * kBatch) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) v[j] = g0 + 32 * j < end ? raw<kResident>(g0 + 32 * j) : nothing();
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (g0 + 32 * j >= end) break;
+        float x[kN];
+        Vec<T>::unpack(v[j], x);
+        f(x, (g0 + 32 * j) * kN - head, g0 + 32 * j);
+      }
     }
-  }
-  // ... and over groups dealt out in turn, where the order does not matter
-  template <bool kResident, class F>
-  __device__ __forceinline__ void any(F f) const {
-#pragma unroll 2
-    for (int g = threadIdx.x; g < groups; g += kThreads) {
-      float x[kN];
-      load<kResident>(g, x);
-      f(x, g * kN - head);
-    }
-  }
-  // logit e of the run that starts at group g0
-  template <bool kResident>
-  __device__ __forceinline__ float at(int g0, int e) const {
-    const int i = g0 * kN - head + e;
-    if (i < 0 || i >= n) return -INFINITY;
-    if (!kResident) return Vec<T>::one(src + i);
-    const T* p = reinterpret_cast<const T*>(stage + g0) + e;
-    if constexpr (sizeof(T) == 4)
-      return *p;
-    else
-      return __bfloat162float(*p);
   }
 };
 
@@ -523,13 +501,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     __syncthreads();
     bool ok = true;
-    const int w0 = warp * 32 * sl.run(), w1 = w0 + 32 * sl.run();  // the warp's groups
+    const int w0 = warp * sl.run(), w1 = w0 + sl.run();  // the warp's groups
     for (int i = w0 / max(piece, 1); i < kPieces && i * piece < w1; ++i) ok &= wait_piece(smem_u32(&s.bar[i]));
     if (!ok && a.status) atomicOr(a.status, SV_DEV_TIMEOUT);
   }
-  // the thread's largest logit (fmaxf passes over NaN)
-  float top_here = -INFINITY;
-  sl.template own<kResident>([&](const float(&x)[kN], int) { top_here = fmaxf(top_here, max_of(x)); });
+  // The thread's largest logit, its group, and the largest of the other groups
+  // (fmaxf passes over NaN): what is kept in the end is mostly a few logits, so
+  // that hardly a thread has to look at its logits again.
+  float top_here = -INFINITY, next_here = -INFINITY;
+  int top_group = 0;
+  sl.template own<kResident, kResident ? 4 : 8>([&](const float(&x)[kN], int, int g) {
+    const float v = max_of(x);
+    next_here = fmaxf(next_here, fminf(v, top_here));
+    if (v > top_here) {
+      top_here = v;
+      top_group = g;
+    }
+  });
+  // f(x[kN], logit of x[0], group) for the thread's groups that may reach `least`
+  auto reaching = [&](float least, auto f) {
+    if (!(top_here >= least)) return;
+    if (next_here < least) {
+      float x[kN];
+      Vec<T>::unpack(sl.template raw<kResident>(top_group), x);
+      f(x, top_group * kN - sl.head, top_group);
+    } else {
+      sl.template own<kResident, 4>([&](const float(&x)[kN], int i0, int g) {
+        if (max_of(x) >= least) f(x, i0, g);
+      });
+    }
+  };
 
   const bool greedy = tau < 5.4210109e-20f;  // 2^-64
   if (greedy) {
@@ -650,17 +651,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (bound > -INFINITY) {
     // ---- small top-k: the candidates decide
     u64 mine[1] = {0};
-    if (top_here >= bound)
-      sl.template own<kResident>([&](const float(&x)[kN], int i0) {
-        if (max_of(x) >= bound) {
+    reaching(bound, [&](const float(&x)[kN], int i0, int) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i)
-            if (x[i] >= bound) {
-              collect(x[i], i0 + i);
-              ++mine[0];
-            }
+      for (int i = 0; i < kN; ++i)
+        if (x[i] >= bound) {
+          collect(x[i], i0 + i);
+          ++mine[0];
         }
-      });
+    });
     __syncwarp();
     const u64(*const counts)[kSlots] = cl.sum(mine);
     const int n = (int)min(mine[0], (u64)kList + 1);
@@ -717,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       __syncthreads();
       // the histogram and, for top-p, the exact weight of all
       u64 all[1] = {0};
-      sl.template any<kResident>([&](const float(&x)[kN], int) {
+      sl.template own<kResident, 2>([&](const float(&x)[kN], int, int) {
         int bin[kN];
         uint32_t one[kN];
 #pragma unroll
@@ -909,8 +907,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         u64 sums[2] = {0, 0};  // above the window, logits in it
         uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
         const unsigned width = (unsigned)(b1 - b0);
-        sl.template any<kResident>([&](const float(&x)[kN], int i0) {
-          if (!(max_of(x) >= edge)) return;
+        reaching(edge, [&](const float(&x)[kN], int i0, int) {
           int b[kN];
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
@@ -949,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           low = key_float(key_min);
           high = key_float(key_max);
           u64 in_bin[1] = {0};
-          sl.template any<kResident>([&](const float(&x)[kN], int) {
+          reaching(low, [&](const float(&x)[kN], int, int) {
 #pragma unroll
             for (int i = 0; i < kN; ++i)
               if (x[i] >= low && x[i] <= high) in_bin[0] += by_weight ? weight(x[i]) : 1;
@@ -994,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const uint32_t mid = from + (to - from) / 2 + 1;
           const float vmid = key_float(mid);
           u64 c[1] = {0};
-          sl.template any<kResident>([&](const float(&x)[kN], int) {
+          reaching(vmid, [&](const float(&x)[kN], int, int) {
 #pragma unroll
             for (int i = 0; i < kN; ++i)
               if (x[i] >= vmid && x[i] <= high) c[0] += by_weight ? weight(x[i]) : 1;
@@ -1012,48 +1009,81 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       theta = fmaxf(theta, border);
     }
 
-    // ---- the draw, in the order of the vocabulary
+    // ---- the draw, in the order of the vocabulary: the warp that holds the
+    // token, then its whole CTA looks at that warp's logits
     u64 mine = 0;
-    if (top_here >= theta)
-      sl.template own<kResident>([&](const float(&x)[kN], int) {
-        if (max_of(x) >= theta) {
+    reaching(theta, [&](const float(&x)[kN], int, int) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const u64 w = weight(x[i]);
-            mine += x[i] >= theta ? w : 0;
-          }
-        }
-      });
+      for (int i = 0; i < kN; ++i) {
+        const u64 w = weight(x[i]);
+        mine += x[i] >= theta ? w : 0;
+      }
+    });
     __syncwarp();
-    const u64 upto = Cluster::warp_scan(mine);  // over the warp
-    const u64 of_warp[1] = {__shfl_sync(0xFFFFFFFFu, upto, 31)};
+    const u64 of_warp[1] = {Cluster::warp_sum(mine)};
     const Cluster::Four f = cl.four(cl.leave(of_warp)[0]);
-    const u64 until = Cluster::warp_scan(f.sum());
+    const u64 until = scan_add(f.sum());
     total = __shfl_sync(0xFFFFFFFFu, until, 31);
     const u64 target = min(__umul64hi(chance, total), total - 1);
-    // the weight before this warp: slot `place`
-    const int sub = cl.place() & 3;
-    const u64 mine4 = until - f.sum() + (sub > 0 ? f.v[0] : 0) + (sub > 1 ? f.v[1] : 0) + (sub > 2 ? f.v[2] : 0);
-    const u64 before = __shfl_sync(0xFFFFFFFFu, mine4, cl.place() >> 2);
-    if (target >= before && target - before < of_warp[0]) {
-      // this warp holds the token: its lane, then the lane's logits side by side
-      const unsigned who = __ballot_sync(0xFFFFFFFFu, before + upto > target);
-      const int l0 = __ffs(who) - 1;
-      u64 run = before + __shfl_sync(0xFFFFFFFFu, upto - mine, l0);
-      const int g0 = (warp * 32 + l0) * sl.run(), n = sl.run() * kN;
-      for (int e0 = 0; e0 < n; e0 += 32) {
-        const int e = e0 + lane;
-        const float x = e < n ? sl.template at<kResident>(g0, e) : -INFINITY;
-        const u64 w = x >= theta ? weight(x) : 0;
-        const u64 incl = run + Cluster::warp_scan(w);
-        if (w != 0 && incl > target && incl - w <= target) {
-          const int token = (int)(lo + g0 * kN - sl.head + e);
+    int at = -1;
+    u64 before = until - f.sum();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (at < 0 && target >= before && target - before < f.v[i]) at = 4 * lane + i;
+      if (at < 0) before += f.v[i];
+    }
+    const int l0 = __ffs(__ballot_sync(0xFFFFFFFFu, at >= 0)) - 1;
+    at = __shfl_sync(0xFFFFFFFFu, at, l0);
+    before = __shfl_sync(0xFFFFFFFFu, before, l0);
+    if (at / kWarps == (int)cl.rank) {
+      const int end = min(sl.groups, (at % kWarps + 1) * sl.run());
+      for (int g0 = at % kWarps * sl.run(); g0 < end; g0 += kThreads * kHold) {
+        // a thread takes up to kHold neighbouring groups
+        const int hold = min(kHold, (end - g0 + kThreads - 1) / kThreads), first = g0 + (int)threadIdx.x * hold;
+        uint4 v[kHold];
+        u64 sum = 0;
+#pragma unroll
+        for (int j = 0; j < kHold; ++j)
+          v[j] = j < hold && first + j < end ? sl.template raw<kResident>(first + j) : Slice<T>::nothing();
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+          float x[kN];
+          Vec<T>::unpack(v[j], x);
+          if (max_of(x) >= theta) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) sum += x[i] >= theta ? weight(x[i]) : 0;
+          }
+        }
+        u64 upto = scan_add(sum);
+        __syncthreads();
+        if (lane == 31) s.weight[warp] = upto;
+        __syncthreads();
+        u64 all = 0;
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) upto += s.weight[w];
+          all += s.weight[w];
+        }
+        upto += before;
+        if (target >= upto - sum && target < upto) {
+          u64 c = upto - sum;
+          int token = -1;
+#pragma unroll
+          for (int j = 0; j < kHold; ++j) {
+            float x[kN];
+            Vec<T>::unpack(v[j], x);
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (x[i] >= theta) {
+                c += weight(x[i]);
+                if (token < 0 && c > target) token = (int)(lo + (first + j) * kN - sl.head + i);
+              }
+          }
           a.tokens[t] = token;
           if (probs && greedy)
             for (uint32_t r = 0; r < cl.size; ++r) cluster_st(cluster_map(&s.token, r), (uint32_t)token);
         }
-        run = __shfl_sync(0xFFFFFFFFu, incl, 31);
-        if (run > target) break;
+        before += all;
+        if (before > target) break;
       }
     }
   }
@@ -1067,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   __syncthreads();
   const float inv = s.delta[0];
   const bool wide = ((reinterpret_cast<uintptr_t>(probs) - 4u * sl.head) & 15u) == 0;  // groups at 16-byte addresses
-  sl.template any<kResident>([&](const float(&x)[kN], int i0) {
+  sl.template own<kResident, 2>([&](const float(&x)[kN], int i0, int) {
     float p[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) p[i] = 0.f;
@@ -1092,26 +1122,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 }
 
 // ------------------------------------------------------------------ host side
-// 228 KB of an SM, 1 KB of it taken per CTA; at most 227 KB for one
-constexpr size_t kStageTwo = (114 * 1024 - 1024 - sizeof(Shared) - 64) / 16 * 16;   // two CTAs of an SM keep their slices
-constexpr size_t kStageOne = (227 * 1024 - sizeof(Shared) - 64) / 16 * 16;          // one CTA does
+// two CTAs share an SM's 228 KB, of which each CTA takes 1 KB more than it asks for
+constexpr size_t kStage = (114 * 1024 - 1024 - sizeof(Shared) - 64) / 16 * 16;
 
 struct Shape {
   int ctas, slice;
   size_t stage;  // bytes of a resident slice, 0: rows are read again for every pass
 };
-// The fewest CTAs a row whose slices fit two to an SM; more where few rows
-// would leave SMs idle (a row's passes get shorter, down to 4096 logits a CTA).
+// As many CTAs a row as keep all rows on the GPU at once (two CTAs an SM),
+// down to 4096 logits a CTA.  With many rows a slice then does not fit in
+// shared memory and is read again where a later pass needs it, mostly from L2:
+// for top-k and min-p that is a few groups (512 rows of 163840 logits, min-p:
+// one CTA a row 0 us, eight CTAs with slices in shared memory 114 us).
 Shape row_shape(int T, int V, int elem) {
   Shape sh;
   auto slice_of = [&](int c) { return (int)((((long long)V + c - 1) / c + 7) / 8 * 8); };
   auto stage_of = [&](int c) { return ((size_t)slice_of(c) * elem + 16 + 15) / 16 * 16; };
   int c = 1;
-  while (c < kClusterMax && stage_of(c) > kStageTwo) c *= 2;
-  while (c < kClusterMax && (long long)T * c < 304 && slice_of(2 * c) >= 4096) c *= 2;
+  while (c < kClusterMax && (long long)T * 2 * c <= 304 && slice_of(2 * c) >= 4096) c *= 2;
   sh.ctas = c;
   sh.slice = slice_of(c);
-  sh.stage = stage_of(c) <= kStageOne ? stage_of(c) : 0;
+  sh.stage = stage_of(c) <= kStage ? stage_of(c) : 0;
   return sh;
 }
 
@@ -1124,7 +1155,7 @@ cudaError_t launch_sample(const SampleArgs& a, int rows, const Shape& sh, cudaSt
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStageOne);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStage);
       if (e != cudaSuccess) return e;
       if (dev < 64) done[dev].store(true, std::memory_order_release);
     }
