@@ -122,6 +122,7 @@ struct SampleArgs {
   double ln_min_p_all;  // ln(min_p_all), 0 above 1
   long long row_stride;
   int V, slice;  // slice: logits per CTA, a multiple of 8
+  int rows, ahead;  // row t + ahead is fetched into L2 early (0: none)
   int down;      // the largest weight is mant << 31 >> down (mant < 2^32): V of them stay below 2^63
   int32_t* tokens;
   float* probs;
@@ -400,22 +401,28 @@ struct Slice {
   }
   // A warp owns a run of consecutive groups, dealt out to its lanes in turn.
   __device__ __forceinline__ int run() const { return (groups + kWarps - 1) / kWarps; }
-  // f(x[kN], logit of the slice of x[0], group) over the thread's groups, kBatch loads at a time
+  // f(x[kN], logit of the slice of x[0], group) over groups g0, g0 + step, ..
+  // below end, kBatch loads at a time; f also sees groups of -inf at the end.
   template <bool kResident, int kBatch, class F>
-  __device__ __forceinline__ void own(F f) const {
-    const int w = (int)threadIdx.x >> 5, end = min(groups, (w + 1) * run());
-    for (int g0 = w * run() + ((int)threadIdx.x & 31); g0 < end; g0 += 32 * kBatch) {
+  __device__ __forceinline__ void walk(int g0, int end, int step, F f) const {
+    for (; g0 < end; g0 += step * kBatch) {
       uint4 v[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) v[j] = g0 + 32 * j < end ? raw<kResident>(g0 + 32 * j) : nothing();
+      for (int j = 0; j < kBatch; ++j) v[j] = g0 + step * j < end ? raw<kResident>(g0 + step * j) : nothing();
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        if (g0 + 32 * j >= end) break;
         float x[kN];
         Vec<T>::unpack(v[j], x);
-        f(x, (g0 + 32 * j) * kN - head, g0 + 32 * j);
+        f(x, (g0 + step * j) * kN - head, g0 + step * j);
       }
     }
+  }
+  __device__ __forceinline__ int run_end() const {
+    return min(groups, (((int)threadIdx.x >> 5) + 1) * run());
+  }
+  template <bool kResident, int kBatch, class F>
+  __device__ __forceinline__ void own(F f) const {
+    walk<kResident, kBatch>(((int)threadIdx.x >> 5) * run() + ((int)threadIdx.x & 31), run_end(), 32, f);
   }
 };
 
@@ -447,6 +454,17 @@ __device__ __forceinline__ bool wait_piece(uint32_t bar) {
   while (!mbar_test(bar, 0))
     if (globaltimer_ns() - t0 >= kWaitTimeoutNs) return false;
   return true;
+}
+
+// The slice `away` elements further on, from HBM into L2: a hint.
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const Slice<T>& sl, long long away) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(sl.src + away);
+  const uintptr_t p0 = (p + 15) & ~(uintptr_t)15, p1 = (p + (size_t)sl.n * sizeof(T)) & ~(uintptr_t)15;
+  constexpr uintptr_t kPart = 16384;
+  const uintptr_t at = p0 + threadIdx.x * kPart;
+  if (at < p1)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"((uint32_t)min(kPart, p1 - at)) : "memory");
 }
 
 template <typename T, bool kResident>
@@ -518,18 +536,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       top_group = g;
     }
   });
-  // f(x[kN], logit of x[0], group) for the thread's groups that may reach `least`
+  // Rows that are not on the GPU yet start on their way into L2 while this one
+  // is past its pass over the logits.
+  if (!kResident && a.ahead > 0 && t + a.ahead < a.rows) prefetch_row<T>(sl, a.ahead * a.row_stride);
+
+  // f(x[kN], logit of x[0]) for the groups of the warp that reach `least`, each
+  // in some lane of it.  Lanes with more than one such group are served by the
+  // whole warp, unless there are many.
   auto reaching = [&](float least, auto f) {
-    if (!(top_here >= least)) return;
-    if (next_here < least) {
-      float x[kN];
-      Vec<T>::unpack(sl.template raw<kResident>(top_group), x);
-      f(x, top_group * kN - sl.head, top_group);
+    const bool more = next_here >= least;
+    const unsigned many = __ballot_sync(0xFFFFFFFFu, more);
+    auto look = [&](const float(&x)[kN], int i0, int) {
+      if (max_of(x) >= least) f(x, i0);
+    };
+    if (__popc(many) > 6) {
+      sl.template own<kResident, 4>(look);
     } else {
-      sl.template own<kResident, 4>([&](const float(&x)[kN], int i0, int g) {
-        if (max_of(x) >= least) f(x, i0, g);
-      });
+      if (top_here >= least && !more) {
+        float x[kN];
+        Vec<T>::unpack(sl.template raw<kResident>(top_group), x);
+        f(x, top_group * kN - sl.head);
+      }
+      for (unsigned left = many; left != 0; left &= left - 1) {
+        const int first = warp * sl.run() + __ffs(left) - 1;
+        sl.template walk<kResident, 3>(first + 32 * lane, sl.run_end(), 1024, look);
+      }
     }
+    __syncwarp();
   };
 
   const bool greedy = tau < 5.4210109e-20f;  // 2^-64
@@ -651,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (bound > -INFINITY) {
     // ---- small top-k: the candidates decide
     u64 mine[1] = {0};
-    reaching(bound, [&](const float(&x)[kN], int i0, int) {
+    reaching(bound, [&](const float(&x)[kN], int i0) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
         if (x[i] >= bound) {
@@ -659,7 +692,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           ++mine[0];
         }
     });
-    __syncwarp();
     const u64(*const counts)[kSlots] = cl.sum(mine);
     const int n = (int)min(mine[0], (u64)kList + 1);
     done = n <= kList;
@@ -907,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         u64 sums[2] = {0, 0};  // above the window, logits in it
         uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
         const unsigned width = (unsigned)(b1 - b0);
-        reaching(edge, [&](const float(&x)[kN], int i0, int) {
+        reaching(edge, [&](const float(&x)[kN], int i0) {
           int b[kN];
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
@@ -934,7 +966,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
               }
             }
         });
-        __syncwarp();
         if (heavy) {
           key_max = cl.max(key_max);
           key_min = ~cl.max(~key_min);
@@ -946,12 +977,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           low = key_float(key_min);
           high = key_float(key_max);
           u64 in_bin[1] = {0};
-          reaching(low, [&](const float(&x)[kN], int, int) {
+          reaching(low, [&](const float(&x)[kN], int) {
 #pragma unroll
             for (int i = 0; i < kN; ++i)
               if (x[i] >= low && x[i] <= high) in_bin[0] += by_weight ? weight(x[i]) : 1;
           });
-          __syncwarp();
           cl.sum(in_bin);
           if (over >= need || over + in_bin[0] < need) {
             low = base;
@@ -991,12 +1021,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           const uint32_t mid = from + (to - from) / 2 + 1;
           const float vmid = key_float(mid);
           u64 c[1] = {0};
-          reaching(vmid, [&](const float(&x)[kN], int, int) {
+          reaching(vmid, [&](const float(&x)[kN], int) {
 #pragma unroll
             for (int i = 0; i < kN; ++i)
               if (x[i] >= vmid && x[i] <= high) c[0] += by_weight ? weight(x[i]) : 1;
           });
-          __syncwarp();
           cl.sum(c);
           if (over + c[0] >= need)
             from = mid;
@@ -1012,14 +1041,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // ---- the draw, in the order of the vocabulary: the warp that holds the
     // token, then its whole CTA looks at that warp's logits
     u64 mine = 0;
-    reaching(theta, [&](const float(&x)[kN], int, int) {
+    reaching(theta, [&](const float(&x)[kN], int) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const u64 w = weight(x[i]);
         mine += x[i] >= theta ? w : 0;
       }
     });
-    __syncwarp();
     const u64 of_warp[1] = {Cluster::warp_sum(mine)};
     const Cluster::Four f = cl.four(cl.leave(of_warp)[0]);
     const u64 until = scan_add(f.sum());
@@ -1097,7 +1125,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   __syncthreads();
   const float inv = s.delta[0];
   const bool wide = ((reinterpret_cast<uintptr_t>(probs) - 4u * sl.head) & 15u) == 0;  // groups at 16-byte addresses
-  sl.template own<kResident, 2>([&](const float(&x)[kN], int i0, int) {
+  const int run_end = sl.run_end();
+  sl.template own<kResident, 2>([&](const float(&x)[kN], int i0, int g) {
+    if (g >= run_end) return;
     float p[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) p[i] = 0.f;
@@ -1217,6 +1247,8 @@ extern "C" sv_status sample_tokens(const void* logits, int logits_type, int T, i
   a.status = status;
   const Shape sh = row_shape(T, V, elem);
   a.slice = sh.slice;
+  a.rows = T;
+  a.ahead = sh.ctas == 1 && T > 304 ? 304 : 0;
   a.down = 0;
   while ((1 << a.down) < V) ++a.down;  // V <= 2^down: V (2^63 >> down) <= 2^63
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
