@@ -408,41 +408,52 @@ def mla_wuv_project(x: torch.Tensor, w_uv: torch.Tensor, out_v: torch.Tensor | N
 
 # ------------------------------------------------------------------ pages of the cache
 # The calls below are short on the GPU (2 to 20 us), so their host time
-# counts: messages are built only where a check fails.
+# counts: checks are plain comparisons, and messages are built only where one
+# fails.
 _INT32, _FP32 = torch.int32, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty_like = torch.empty_like
 
 
-def _launch(func: str, dev: torch.device, *args):
+def _launch(func: str, index: int, *args):
     """Call the library with the tensors' device current (launches go there)."""
-    f = getattr(load_library(), func)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        code = f(*args, _stream(dev))
+    f = getattr(_lib or load_library(), func)
+    if index == torch._C._cuda_getDevice():
+        code = f(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            code = f(*args, _stream(dev))
+        with torch.cuda.device(index):
+            code = f(*args, _raw_stream(index))
     if code != 0:
         raise SpecVerifyError(func, code)
 
 
-def _vector(name: str, t: torch.Tensor, dtype: torch.dtype, dev: torch.device, n: int):
-    if t.dtype is not dtype or t.device != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name}: {dtype}, contiguous, [{n}] on {dev}")
+def _index(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return index
+
+
+def _vector(name: str, t: torch.Tensor, dtype: torch.dtype, index: int, n: int) -> int:
+    if t.dtype is not dtype or t.get_device() != index or t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: {dtype}, contiguous, [{n}] on cuda:{index}")
     return t.data_ptr()
 
 
 def _result(name: str, out: torch.Tensor | None, like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty_like(like)
-    if out.dtype is not like.dtype or out.device != like.device or out.shape != like.shape or not out.is_contiguous():
+        return _empty_like(like)
+    if out.dtype is not like.dtype or out.get_device() != like.get_device() or out.shape != like.shape \
+            or not out.is_contiguous():
         raise ValueError(f"{name}: {like.dtype}, contiguous, {tuple(like.shape)} on {like.device}")
     return out
 
 
-def _status_ptr(status: torch.Tensor | None, dev: torch.device):
+def _status_ptr(status: torch.Tensor | None, index: int):
     if status is None:
         return None
-    if status.dtype is not _INT32 or status.device != dev or status.numel() < 1:
-        raise ValueError(f"status: int32 on {dev}")
+    if status.dtype is not _INT32 or status.get_device() != index or status.numel() < 1:
+        raise ValueError(f"status: int32 on cuda:{index}")
     return status.data_ptr()
 
 
@@ -453,37 +464,38 @@ def kv_pages_workspace_bytes(num_pages: int, R: int, n: int = 0) -> int:
     return int(load_library().sv_kv_pages_workspace_bytes(num_pages, R, n))
 
 
-def _pages_workspace(dev: torch.device, workspace: torch.Tensor | None, need: int) -> torch.Tensor:
+def _pages_workspace(like: torch.Tensor, workspace: torch.Tensor | None, need: int) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace: contiguous, on {dev}")
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous, on {like.device}")
     return workspace
 
 
 def _pool_shape(name: str, t: torch.Tensor):
     """(layers, pages, bytes of a row) of [P, 64, W] or [layers, P, 64, W]."""
     shape = t.shape
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    if len(shape) not in (3, 4) or shape[-2] != SV_PAGE_SIZE or not t.is_contiguous():
+    if len(shape) == 4:
+        layers, pages, rows, width = shape
+    elif len(shape) == 3:
+        layers, (pages, rows, width) = 1, shape
+    else:
+        rows = 0
+    if rows != SV_PAGE_SIZE or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, [P, 64, W] or [layers, P, 64, W]")
-    return (shape[0] if len(shape) == 4 else 1), shape[-3], shape[-1] * t.element_size()
+    return layers, pages, width * t.element_size()
 
 
 def _tables(ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor):
-    """(device, P, R, max_pages, the three pointers)"""
-    dev = ref_counts.device
-    if not ref_counts.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    if ref_counts.dim() != 1:
-        raise ValueError("ref_counts must be [P]")
-    P = ref_counts.shape[0]
-    refs = _vector("ref_counts", ref_counts, _INT32, dev, P)
-    if block_table.dtype is not _INT32 or block_table.device != dev or block_table.dim() != 2 or not block_table.is_contiguous():
-        raise ValueError(f"block_table: int32, contiguous, [R, max_pages] on {dev}")
+    """(device index, P, R, max_pages, the three pointers)"""
+    index = _index(ref_counts)
+    if block_table.dtype is not _INT32 or block_table.get_device() != index or block_table.dim() != 2 \
+            or not block_table.is_contiguous():
+        raise ValueError(f"block_table: int32, contiguous, [R, max_pages] on cuda:{index}")
+    P = ref_counts.numel()
     R, max_pages = block_table.shape
-    return dev, P, R, max_pages, (refs, block_table.data_ptr(), _vector("kv_lens", kv_lens, _INT32, dev, R))
+    return index, P, R, max_pages, (_vector("ref_counts", ref_counts, _INT32, index, P), block_table.data_ptr(),
+                                    _vector("kv_lens", kv_lens, _INT32, index, R))
 
 
 def kv_pages_copy(src_pages: torch.Tensor, dst_pages: torch.Tensor, src_ids: torch.Tensor, dst_ids: torch.Tensor,
@@ -492,17 +504,15 @@ def kv_pages_copy(src_pages: torch.Tensor, dst_pages: torch.Tensor, src_ids: tor
     (in place), in every layer.  The pools are [P, 64, W] or [layers, P, 64, W]
     and may be one tensor; an id of -1 skips the pair.  Destinations must be
     distinct and, in one pool, no source of the call."""
+    index = _index(dst_pages)
     layers, src_p, row = _pool_shape("src_pages", src_pages)
     dst_layers, dst_p, dst_row = _pool_shape("dst_pages", dst_pages)
-    dev = dst_pages.device
-    if src_pages.device != dev:
-        raise ValueError(f"src_pages must be on {dev}")
-    if src_pages.dtype is not dst_pages.dtype or layers != dst_layers or row != dst_row:
-        raise ValueError("the pools must have the same type, layers and row width")
+    if src_pages.get_device() != index or src_pages.dtype is not dst_pages.dtype or layers != dst_layers or row != dst_row:
+        raise ValueError("the pools must be on one device and have the same type, layers and row width")
     n = src_ids.numel()
-    _launch("kv_pages_copy", dev, src_pages.data_ptr(), src_p, dst_pages.data_ptr(), dst_p, layers, row * SV_PAGE_SIZE,
-            _vector("src_ids", src_ids, _INT32, dev, n), _vector("dst_ids", dst_ids, _INT32, dev, n), n,
-            _status_ptr(status, dev))
+    _launch("kv_pages_copy", index, src_pages.data_ptr(), src_p, dst_pages.data_ptr(), dst_p, layers, row * SV_PAGE_SIZE,
+            _vector("src_ids", src_ids, _INT32, index, n), _vector("dst_ids", dst_ids, _INT32, index, n), n,
+            _status_ptr(status, index))
     return dst_pages
 
 
@@ -514,18 +524,19 @@ def kv_pages_fork(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_table:
     parent's full pages and gets a copy of its last, partly filled one in
     kv_pages (in place).  Returns (ref_counts, block_table, kv_lens) after the
     forks, in new tensors or in the *_out tensors, which may be the inputs."""
-    dev, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
+    index, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
     layers, pages, row = _pool_shape("kv_pages", kv_pages)
-    if pages != P or kv_pages.device != dev:
-        raise ValueError(f"kv_pages must have ref_counts' {P} pages, on {dev}")
+    if pages != P or kv_pages.get_device() != index:
+        raise ValueError(f"kv_pages must have ref_counts' {P} pages, on cuda:{index}")
     n = parents.numel()
-    forks = _vector("parents", parents, _INT32, dev, n), _vector("children", children, _INT32, dev, n)
-    outs = (_result("ref_counts_out", ref_counts_out, ref_counts), _result("block_table_out", block_table_out, block_table),
-            _result("kv_lens_out", kv_lens_out, kv_lens))
-    ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R, n))
-    _launch("kv_pages_fork", dev, kv_pages.data_ptr(), P, SV_PAGE_SIZE, layers, row, *ptrs, R, max_pages, *forks, n,
-            outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), ws.data_ptr(), ws.nbytes, _status_ptr(status, dev))
-    return outs
+    forks = _vector("parents", parents, _INT32, index, n), _vector("children", children, _INT32, index, n)
+    refs = _result("ref_counts_out", ref_counts_out, ref_counts)
+    table = _result("block_table_out", block_table_out, block_table)
+    lens = _result("kv_lens_out", kv_lens_out, kv_lens)
+    ws = _pages_workspace(ref_counts, workspace, kv_pages_workspace_bytes(P, R, n))
+    _launch("kv_pages_fork", index, kv_pages.data_ptr(), P, SV_PAGE_SIZE, layers, row, *ptrs, R, max_pages, *forks, n,
+            refs.data_ptr(), table.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.nbytes, _status_ptr(status, index))
+    return refs, table, lens
 
 
 def kv_pages_resize(ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, new_lens: torch.Tensor,
@@ -535,14 +546,15 @@ def kv_pages_resize(ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens
     """Give request r the pages of length new_lens[r] (-1: as it is, 0: none),
     handing out the lowest free pages and taking back those behind the new
     length.  Returns (ref_counts, block_table, kv_lens) as kv_pages_fork."""
-    dev, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
-    new = _vector("new_lens", new_lens, _INT32, dev, R)
-    outs = (_result("ref_counts_out", ref_counts_out, ref_counts), _result("block_table_out", block_table_out, block_table),
-            _result("kv_lens_out", kv_lens_out, kv_lens))
-    ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R))
-    _launch("kv_pages_resize", dev, ptrs[0], P, SV_PAGE_SIZE, ptrs[1], ptrs[2], R, max_pages, new, outs[0].data_ptr(),
-            outs[1].data_ptr(), outs[2].data_ptr(), ws.data_ptr(), ws.nbytes, _status_ptr(status, dev))
-    return outs
+    index, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
+    new = _vector("new_lens", new_lens, _INT32, index, R)
+    refs = _result("ref_counts_out", ref_counts_out, ref_counts)
+    table = _result("block_table_out", block_table_out, block_table)
+    lens = _result("kv_lens_out", kv_lens_out, kv_lens)
+    ws = _pages_workspace(ref_counts, workspace, kv_pages_workspace_bytes(P, R))
+    _launch("kv_pages_resize", index, ptrs[0], P, SV_PAGE_SIZE, ptrs[1], ptrs[2], R, max_pages, new, refs.data_ptr(),
+            table.data_ptr(), lens.data_ptr(), ws.data_ptr(), ws.nbytes, _status_ptr(status, index))
+    return refs, table, lens
 
 
 def kv_pages_compact(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -552,24 +564,30 @@ def kv_pages_compact(kv_pages: torch.Tensor, ref_counts: torch.Tensor, block_tab
     """Move the pages in use to the front of kv_pages (in place).  Returns
     (ref_counts, block_table, page_map [P]: every page's new id or -1,
     num_live [1]); the *_out tensors may be the inputs."""
-    dev, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
+    index, P, R, max_pages, ptrs = _tables(ref_counts, block_table, kv_lens)
     layers, pages, row = _pool_shape("kv_pages", kv_pages)
-    if pages != P or kv_pages.device != dev:
-        raise ValueError(f"kv_pages must have ref_counts' {P} pages, on {dev}")
-    outs = (_result("ref_counts_out", ref_counts_out, ref_counts), _result("block_table_out", block_table_out, block_table),
-            _result("page_map", page_map, ref_counts))
+    if pages != P or kv_pages.get_device() != index:
+        raise ValueError(f"kv_pages must have ref_counts' {P} pages, on cuda:{index}")
+    refs = _result("ref_counts_out", ref_counts_out, ref_counts)
+    table = _result("block_table_out", block_table_out, block_table)
+    page_map = _result("page_map", page_map, ref_counts)
     if num_live is None:
-        num_live = torch.empty(1, dtype=_INT32, device=dev)
-    live = _vector("num_live", num_live, _INT32, dev, 1)
-    ws = _pages_workspace(dev, workspace, kv_pages_workspace_bytes(P, R))
-    _launch("kv_pages_compact", dev, kv_pages.data_ptr(), P, SV_PAGE_SIZE, layers, row, *ptrs, R, max_pages,
-            outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), live, ws.data_ptr(), ws.nbytes,
-            _status_ptr(status, dev))
-    return (*outs, num_live)
+        num_live = torch.empty(1, dtype=_INT32, device=ref_counts.device)
+    live = _vector("num_live", num_live, _INT32, index, 1)
+    ws = _pages_workspace(ref_counts, workspace, kv_pages_workspace_bytes(P, R))
+    _launch("kv_pages_compact", index, kv_pages.data_ptr(), P, SV_PAGE_SIZE, layers, row, *ptrs, R, max_pages,
+            refs.data_ptr(), table.data_ptr(), page_map.data_ptr(), live, ws.data_ptr(), ws.nbytes,
+            _status_ptr(status, index))
+    return refs, table, page_map, num_live
 
 
 # ------------------------------------------------------------------ sampling
 _LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _setting(name: str, v, dtype: torch.dtype, index: int, T: int):
+    """(pointer, value) of a setting that is one number or a tensor [T]."""
+    return (_vector(name, v, dtype, index, T), 0) if isinstance(v, torch.Tensor) else (None, v)
 
 
 def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
@@ -583,9 +601,7 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0,
     kind = _LOGITS_TYPES.get(logits.dtype)
     if kind is None or logits.dim() != 2:
         raise ValueError("logits must be [T, V], fp32 or bf16")
-    dev = logits.device
-    if not logits.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
+    index = _index(logits)
     T, V = logits.shape
     row, col = logits.stride()
     if col != 1 and V > 1:
@@ -594,18 +610,16 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0,
         row = V
     elif row < V:
         raise ValueError("rows of logits must not overlap")
-    settings = []
-    for name, v, dtype in (("temperature", temperature, _FP32), ("top_k", top_k, _INT32), ("top_p", top_p, _FP32),
-                           ("min_p", min_p, _FP32)):
-        settings += (_vector(name, v, dtype, dev, T), 0) if isinstance(v, torch.Tensor) else (None, v)
     if tokens is None:
-        tokens = torch.empty(T, dtype=_INT32, device=dev)
+        tokens = torch.empty(T, dtype=_INT32, device=logits.device)
     if probs is None:
         if return_probs:
-            probs = torch.empty((T, V), dtype=_FP32, device=dev)
-    elif probs.dtype is not _FP32 or probs.device != dev or probs.shape != logits.shape or not probs.is_contiguous():
-        raise ValueError(f"probs: fp32, contiguous, [{T}, {V}] on {dev}")
-    _launch("sample_tokens", dev, logits.data_ptr(), kind, T, V, row, _vector("uniforms", uniforms, _FP32, dev, T),
-            *settings, _vector("tokens", tokens, _INT32, dev, T), None if probs is None else probs.data_ptr(),
-            _status_ptr(status, dev))
+            probs = torch.empty((T, V), dtype=_FP32, device=logits.device)
+    elif probs.dtype is not _FP32 or probs.get_device() != index or probs.shape != logits.shape or not probs.is_contiguous():
+        raise ValueError(f"probs: fp32, contiguous, [{T}, {V}] on cuda:{index}")
+    _launch("sample_tokens", index, logits.data_ptr(), kind, T, V, row, _vector("uniforms", uniforms, _FP32, index, T),
+            *_setting("temperature", temperature, _FP32, index, T), *_setting("top_k", top_k, _INT32, index, T),
+            *_setting("top_p", top_p, _FP32, index, T), *_setting("min_p", min_p, _FP32, index, T),
+            _vector("tokens", tokens, _INT32, index, T), None if probs is None else probs.data_ptr(),
+            _status_ptr(status, index))
     return tokens if probs is None else (tokens, probs)

@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kMetaThreads = 1024;
 constexpr int kMetaWarps = kMetaThreads / 32;
+static_assert(kMetaWarps == 32, "the scans below add up 32 warps, and one warp per item of a tile");
 constexpr int kItems = 8;                            // pages per thread and tile
 constexpr int kTile = kMetaThreads * kItems;         // pages per CTA and tile
 constexpr int kClusterMax = 8;
@@ -38,7 +39,8 @@ constexpr int kClusterMax = 8;
 constexpr long long kOneCtaWords = 16384;
 constexpr int kAhead = 8;                            // loads of a thread under way at once
 constexpr int kCopyThreads = 256;
-constexpr int kChunkBytes = kCopyThreads * 16 * 4;   // one CTA pass: four 16-byte words per thread
+constexpr int kChunkWords = 8;                       // 16-byte words of a chunk per thread
+constexpr int kChunkBytes = kCopyThreads * 16 * kChunkWords;
 
 struct MetaShared {
   int seg[kItems * kMetaWarps];
@@ -191,6 +193,23 @@ __device__ __forceinline__ void copy_words(int32_t* to, const int32_t* from, lon
   }
 }
 
+// Entries j .. j+3 of a row of n (with `wide` the row is 16-byte aligned and n a
+// multiple of 4); what is past the end reads as -1 and is not written.
+__device__ __forceinline__ int4 load_four(const int32_t* row, int j, int n, bool wide) {
+  if (wide) return j < n ? *reinterpret_cast<const int4*>(row + j) : make_int4(-1, -1, -1, -1);
+  return make_int4(j < n ? row[j] : -1, j + 1 < n ? row[j + 1] : -1, j + 2 < n ? row[j + 2] : -1, j + 3 < n ? row[j + 3] : -1);
+}
+__device__ __forceinline__ void store_four(int32_t* row, int j, int n, bool wide, int4 v) {
+  if (wide) {
+    if (j < n) *reinterpret_cast<int4*>(row + j) = v;
+    return;
+  }
+  if (j < n) row[j] = v.x;
+  if (j + 1 < n) row[j + 1] = v.y;
+  if (j + 2 < n) row[j + 2] = v.z;
+  if (j + 3 < n) row[j + 3] = v.w;
+}
+
 __device__ __forceinline__ Group make_group() { return Group{cluster_rank(), cluster_size(), 0}; }
 
 // ---------------------------------------------------------------------------
@@ -201,6 +220,7 @@ struct ResizeArgs {
   int32_t *ref_out, *table_out, *lens_out, *status;
   int *prefix, *list;  // workspace: pages asked for before request r; free pages
   int P, R, mp;
+  bool wide;  // the tables' rows are 16-byte aligned and a multiple of 16 bytes long
 };
 
 struct Change {
@@ -208,17 +228,20 @@ struct Change {
   int have, want;  // entries held before and after
   int old_len, new_len;
 };
-__device__ __forceinline__ Change read_change(const ResizeArgs& a, int r, bool tell) {
+__device__ __forceinline__ Change change_of(const ResizeArgs& a, int old_len, int new_len, bool tell) {
   Change c;
   const int cap = a.mp * SV_PAGE_SIZE;
-  c.old_len = a.lens_in[r];
-  c.new_len = __ldg(a.new_lens + r);
+  c.old_len = old_len;
+  c.new_len = new_len;
   const bool bad = c.old_len < 0 || c.old_len > cap || c.new_len < -1 || c.new_len > cap;
   if (bad && tell) report(a.status, SV_DEV_BAD_BOUND);
   c.apply = !bad && c.new_len >= 0;
   c.have = c.apply ? (c.old_len + SV_PAGE_SIZE - 1) / SV_PAGE_SIZE : 0;
   c.want = c.apply ? (c.new_len + SV_PAGE_SIZE - 1) / SV_PAGE_SIZE : 0;
   return c;
+}
+__device__ __forceinline__ Change read_change(const ResizeArgs& a, int r, bool tell) {
+  return change_of(a, a.lens_in[r], __ldg(a.new_lens + r), tell);
 }
 // A longer request writes behind its last row: refused where that row's page
 // is held by others too, or is no page (counts after everything was taken
@@ -244,32 +267,68 @@ __global__ void __launch_bounds__(kMetaThreads) resize_kernel(const ResizeArgs a
     copy_words(a.ref_out, a.ref_in, a.P, tid, threads);
     group_sync(g);
   }
-  // take back: a warp per request
-  for (int r = tid >> 5; r < a.R; r += threads >> 5) {
-    const Change c = read_change(a, r, lane == 0);
-    const long long row = (long long)r * a.mp;
+  // Take back: a warp per 128 entries of a row, kUnits of them at a time from
+  // rows far apart (the requests that finish give back hundreds of pages each,
+  // the others none), so that the round trips of lengths, entries and counts
+  // are paid once for all of them.
+  {
+    constexpr int kUnits = 4;
     const bool in_place = a.table_out == a.table_in;
-    for (int j0 = in_place ? c.want / 32 * 32 : 0; j0 < (in_place ? c.have : a.mp); j0 += 32 * kAhead) {
-      int p[kAhead];
+    const int per_row = (a.mp + 127) / 128, units = a.R * per_row, warps = threads >> 5;
+    for (int u0 = tid >> 5; u0 < units; u0 += warps * kUnits) {
+      int row[kUnits], at[kUnits], want[kUnits], have[kUnits], old_len[kUnits], new_len[kUnits];
+      int4 v[kUnits];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = j0 + 32 * i + lane;
-        p[i] = j < a.mp ? a.table_in[row + j] : -1;
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = u0 + warps * i, r = u / per_row;
+        row[i] = u < units ? r : -1;
+        at[i] = (u - r * per_row) * 128 + 4 * lane;
+        old_len[i] = new_len[i] = 0;
+        if (u < units) {
+          old_len[i] = a.lens_in[r];
+          new_len[i] = __ldg(a.new_lens + r);
+          if (!in_place) v[i] = load_four(a.table_in + (long long)r * a.mp, at[i], a.mp, a.wide);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = j0 + 32 * i + lane;
-        const bool drop = j >= c.want && j < c.have;
-        if (drop) {
-          if (p[i] < 0 || p[i] >= a.P) {
-            report(a.status, SV_DEV_BAD_PAGE);
-          } else if (atomicSub(a.ref_out + p[i], 1) <= 0) {
-            atomicAdd(a.ref_out + p[i], 1);  // held by nobody: stays as it was
+      for (int i = 0; i < kUnits; ++i) {
+        const Change c = change_of(a, old_len[i], new_len[i], row[i] >= 0 && at[i] == 0);
+        want[i] = c.want;
+        have[i] = c.have;
+      }
+      if (in_place) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+          if (row[i] >= 0 && at[i] < have[i] && at[i] + 3 >= want[i])
+            v[i] = load_four(a.table_in + (long long)row[i] * a.mp, at[i], a.mp, a.wide);
+      }
+      int old[kUnits][4];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          old[i][k] = 1;
+          if (at[i] + k >= want[i] && at[i] + k < have[i])
+            old[i][k] = p[k] >= 0 && p[k] < a.P ? atomicSub(a.ref_out + p[k], 1) : 0;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        if (row[i] < 0) continue;
+        int p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        int32_t* const out = a.table_out + (long long)row[i] * a.mp;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (at[i] + k < want[i] || at[i] + k >= have[i]) continue;
+          if (old[i][k] <= 0) {
+            if (p[k] >= 0 && p[k] < a.P) atomicAdd(a.ref_out + p[k], 1);  // held by nobody: stays as it was
             report(a.status, SV_DEV_BAD_PAGE);
           }
-          p[i] = -1;
+          p[k] = -1;
+          if (in_place) out[at[i] + k] = -1;
         }
-        if (j < a.mp && (drop || !in_place)) a.table_out[row + j] = p[i];
+        if (!in_place) store_four(out, at[i], a.mp, a.wide, make_int4(p[0], p[1], p[2], p[3]));
       }
     }
   }
@@ -511,12 +570,12 @@ __device__ __forceinline__ void copy_chunk(const uint8_t* src, uint8_t* dst, int
   const uint4* s = reinterpret_cast<const uint4*>(src);
   uint4* d = reinterpret_cast<uint4*>(dst);
   const int words = bytes >> 4;
-  uint4 v[4];
+  uint4 v[kChunkWords];
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+  for (int u = 0; u < kChunkWords; ++u)
     if ((int)threadIdx.x + u * kCopyThreads < words) v[u] = __ldcs(s + threadIdx.x + u * kCopyThreads);
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+  for (int u = 0; u < kChunkWords; ++u)
     if ((int)threadIdx.x + u * kCopyThreads < words) __stcs(d + threadIdx.x + u * kCopyThreads, v[u]);
 }
 
@@ -641,11 +700,13 @@ cudaError_t launch_meta(void (*kernel)(Args), const Args& a, long long words, cu
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// A chunk per CTA: 256 pages of 64 KB in 24 layers (805 MB of traffic) take 121
-// us so, 6.65 TB/s as a plain device copy does, against 131 us for 1216
-// resident CTAs that loop over the chunks and 123-135 us for rings of bulk
-// copies.  Where the number of moves is only known on the device the grid is
-// for at most kMoveCtas of them, the rest by looping.
+// A chunk of 32 KB per CTA: 256 pages of 64 KB in 24 layers (805 MB of traffic)
+// take 121 us so, 6.65 TB/s as a plain device copy does, against 131 us for
+// 1216 resident CTAs that loop over the chunks and 123-135 us for rings of
+// bulk copies.  Chunks of 16 KB do the same here, but lose 2 us where every
+// CTA first reads what it is to move (64 tails in 24 layers: 22.7 against 20.7
+// us).  Where the number of moves is only known on the device the grid is for
+// at most kMoveCtas of them, the rest by looping.
 constexpr long long kMostCtas = 0x7FFFFFFF;
 constexpr long long kMoveCtas = 152 * 8 * 24;
 
@@ -746,6 +807,7 @@ extern "C" sv_status kv_pages_resize(const int32_t* ref_counts_in, int num_pages
   a.P = num_pages;
   a.R = R;
   a.mp = max_pages_per_req;
+  a.wide = max_pages_per_req % 4 == 0 && !off_by(block_table_in, 16) && !off_by(block_table_out, 16);
   return launched(launch_meta(resize_kernel, a, num_pages + (long long)R * max_pages_per_req,
                               reinterpret_cast<cudaStream_t>(stream)));
 }
