@@ -315,8 +315,8 @@ sv_status mla_kv_append(const void* kv_new, const int32_t* positions, const int3
  * kv_pages_resize, kv_pages_compact
  *
  * State, all of it the caller's device memory:
- *   ref_counts   int32 [num_pages]: how many table entries hold the page.  A
- *                page is free exactly when its count is 0; there is no other
+ *   ref_counts   int32 [num_pages], >= 0: how many table entries hold the page.
+ *                A page is free exactly when its count is 0; there is no other
  *                allocator state, so a pool starts with all counts 0.
  *   block_table  int32 [R][max_pages_per_req], as the attention reads it.
  *   kv_lens      int32 [R]: request r holds the first ceil(kv_lens[r] / 64)
@@ -340,8 +340,8 @@ sv_status mla_kv_append(const void* kv_new, const int32_t* positions, const int3
  *              the same time need their own.
  *   status     device int32, may be NULL; ORed with
  *                SV_DEV_BAD_BOUND    a length outside [0, max_pages_per_req*64]
- *                SV_DEV_BAD_PAGE     an entry outside the pool, or one given
- *                                    back that nobody held (that count stays)
+ *                SV_DEV_BAD_PAGE     an entry outside the pool, or a page given
+ *                                    back more often than held (it is free)
  *                SV_DEV_NO_PAGE, SV_DEV_SHARED_PAGE, SV_DEV_BAD_REQUEST
  *              What a bit reports is left undone for that request (fork,
  *              pair) only, as said at each call; the rest is done.

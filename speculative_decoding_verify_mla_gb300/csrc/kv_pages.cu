@@ -153,20 +153,36 @@ __device__ __forceinline__ int tile_rank(Group& g, MetaShared& s, const bool (&f
   return all;
 }
 
+__device__ __forceinline__ void report(int32_t* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
 // The first `want` free pages in ascending order into list[0..); returns how
 // many there are, at most the count at which the search stopped (>= want).
-__device__ int list_free(Group& g, MetaShared& s, const int32_t* ref_counts, int P, int want, int* list) {
+// With kMend all counts are looked at, and one below 0 becomes 0.
+template <bool kMend>
+__device__ int list_free(Group& g, MetaShared& s, int32_t* ref_counts, int P, int want, int* list, int32_t* status) {
   int found = 0;
   const long long step = (long long)kTile * g.size;
-  for (long long base = 0; base < P && found < want; base += step) {
+  for (long long base = 0; base < P && (kMend || found < want); base += step) {
     bool flag[kItems];
-    int rank[kItems];
+    int rank[kItems], ref[kItems];
     const long long p0 = base + (long long)g.rank * kTile + threadIdx.x;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
       const long long p = p0 + k * kMetaThreads;
-      flag[k] = p < P && __ldcg(ref_counts + p) == 0;
+      ref[k] = p < P ? __ldcg(ref_counts + p) : 1;
     }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      flag[k] = ref[k] == 0;
+      if (kMend && ref[k] < 0) {
+        flag[k] = true;
+        ref_counts[p0 + k * kMetaThreads] = 0;
+        report(status, SV_DEV_BAD_PAGE);
+      }
+    }
+    if (found >= want) continue;  // only looking for those now
     const int all = tile_rank(g, s, flag, rank);
 #pragma unroll
     for (int k = 0; k < kItems; ++k)
@@ -174,10 +190,6 @@ __device__ int list_free(Group& g, MetaShared& s, const int32_t* ref_counts, int
     found += all;
   }
   return found;
-}
-
-__device__ __forceinline__ void report(int32_t* status, int bit) {
-  if (status) atomicOr(status, bit);
 }
 
 // n words by `threads` threads, several loads of each under way at once.
@@ -263,74 +275,71 @@ __global__ void __launch_bounds__(kMetaThreads) resize_kernel(const ResizeArgs a
   Group g = make_group();
   const int lane = threadIdx.x & 31;
   const int threads = (int)g.size * kMetaThreads, tid = (int)g.rank * kMetaThreads + threadIdx.x;
+  // Take back: a warp per 128 entries of a row, kUnits of them at a time from
+  // rows far apart (the requests that finish give back hundreds of pages each,
+  // the others none), so that the round trips of lengths, entries and counts
+  // are paid once for all of them.  The first loads go out before the barrier
+  // behind the copy of the counts.
+  constexpr int kUnits = 4;
+  const bool in_place = a.table_out == a.table_in;
+  const int per_row = (a.mp + 127) / 128, units = a.R * per_row, warps = threads >> 5;
+  int u0 = tid >> 5;
+  int row[kUnits], at[kUnits], want[kUnits], have[kUnits];
+  int4 v[kUnits];
+  auto load = [&]() {
+    int old_len[kUnits], new_len[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = u0 + warps * i, r = u / max(per_row, 1);
+      row[i] = u < units ? r : -1;
+      at[i] = (u - r * per_row) * 128 + 4 * lane;
+      old_len[i] = new_len[i] = 0;
+      if (u < units) {
+        old_len[i] = a.lens_in[r];
+        new_len[i] = __ldg(a.new_lens + r);
+        if (!in_place) v[i] = load_four(a.table_in + (long long)r * a.mp, at[i], a.mp, a.wide);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const Change c = change_of(a, old_len[i], new_len[i], row[i] >= 0 && at[i] == 0);
+      want[i] = c.want;
+      have[i] = c.have;
+    }
+    if (in_place) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+        if (row[i] >= 0 && at[i] < have[i] && at[i] + 3 >= want[i])
+          v[i] = load_four(a.table_in + (long long)row[i] * a.mp, at[i], a.mp, a.wide);
+    }
+  };
+  load();
   if (a.ref_out != a.ref_in) {
     copy_words(a.ref_out, a.ref_in, a.P, tid, threads);
     group_sync(g);
   }
-  // Take back: a warp per 128 entries of a row, kUnits of them at a time from
-  // rows far apart (the requests that finish give back hundreds of pages each,
-  // the others none), so that the round trips of lengths, entries and counts
-  // are paid once for all of them.
-  {
-    constexpr int kUnits = 4;
-    const bool in_place = a.table_out == a.table_in;
-    const int per_row = (a.mp + 127) / 128, units = a.R * per_row, warps = threads >> 5;
-    for (int u0 = tid >> 5; u0 < units; u0 += warps * kUnits) {
-      int row[kUnits], at[kUnits], want[kUnits], have[kUnits], old_len[kUnits], new_len[kUnits];
-      int4 v[kUnits];
+  while (u0 < units) {
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + warps * i, r = u / per_row;
-        row[i] = u < units ? r : -1;
-        at[i] = (u - r * per_row) * 128 + 4 * lane;
-        old_len[i] = new_len[i] = 0;
-        if (u < units) {
-          old_len[i] = a.lens_in[r];
-          new_len[i] = __ldg(a.new_lens + r);
-          if (!in_place) v[i] = load_four(a.table_in + (long long)r * a.mp, at[i], a.mp, a.wide);
-        }
+    for (int i = 0; i < kUnits; ++i) {
+      if (row[i] < 0) continue;
+      int p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      int32_t* const out = a.table_out + (long long)row[i] * a.mp;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (at[i] + k < want[i] || at[i] + k >= have[i]) continue;
+        // nobody waits for the answer: a page given back once too often is
+        // seen (below 0) when the free pages are looked up
+        if (p[k] >= 0 && p[k] < a.P)
+          atomicSub(a.ref_out + p[k], 1);
+        else
+          report(a.status, SV_DEV_BAD_PAGE);
+        p[k] = -1;
+        if (in_place) out[at[i] + k] = -1;
       }
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const Change c = change_of(a, old_len[i], new_len[i], row[i] >= 0 && at[i] == 0);
-        want[i] = c.want;
-        have[i] = c.have;
-      }
-      if (in_place) {
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i)
-          if (row[i] >= 0 && at[i] < have[i] && at[i] + 3 >= want[i])
-            v[i] = load_four(a.table_in + (long long)row[i] * a.mp, at[i], a.mp, a.wide);
-      }
-      int old[kUnits][4];
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          old[i][k] = 1;
-          if (at[i] + k >= want[i] && at[i] + k < have[i])
-            old[i][k] = p[k] >= 0 && p[k] < a.P ? atomicSub(a.ref_out + p[k], 1) : 0;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        if (row[i] < 0) continue;
-        int p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        int32_t* const out = a.table_out + (long long)row[i] * a.mp;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (at[i] + k < want[i] || at[i] + k >= have[i]) continue;
-          if (old[i][k] <= 0) {
-            if (p[k] >= 0 && p[k] < a.P) atomicAdd(a.ref_out + p[k], 1);  // held by nobody: stays as it was
-            report(a.status, SV_DEV_BAD_PAGE);
-          }
-          p[k] = -1;
-          if (in_place) out[at[i] + k] = -1;
-        }
-        if (!in_place) store_four(out, at[i], a.mp, a.wide, make_int4(p[0], p[1], p[2], p[3]));
-      }
+      if (!in_place) store_four(out, at[i], a.mp, a.wide, make_int4(p[0], p[1], p[2], p[3]));
     }
+    u0 += warps * kUnits;
+    if (u0 < units) load();
   }
   group_sync(g);
   // rank the needs in request order (every CTA the same sums, rank 0 writes)
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(kMetaThreads) resize_kernel(const ResizeArgs a
     if (r < a.R && g.rank == 0) a.prefix[r] = asked + before;
     asked += total;
   }
-  const int found = list_free(g, s, a.ref_out, a.P, asked, a.list);
+  const int found = list_free<true>(g, s, a.ref_out, a.P, asked, a.list, a.status);
   group_sync(g);
   // hand out: a warp per request
   for (int r = tid >> 5; r < a.R; r += threads >> 5) {
@@ -437,7 +446,7 @@ __global__ void __launch_bounds__(kMetaThreads) fork_kernel(const ForkArgs a) {
     asked += total;
   }
   // the free pages as they were before the call: counts only grow below
-  const int found = list_free(g, s, a.ref_out, a.P, asked, a.list);
+  const int found = list_free<false>(g, s, a.ref_out, a.P, asked, a.list, a.status);
   if (a.lens_out != a.lens_in)
     for (int r = tid; r < a.R; r += threads) a.lens_out[r] = a.lens_in[r];
   group_sync(g);
