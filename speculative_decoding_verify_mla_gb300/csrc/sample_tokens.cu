@@ -131,7 +131,7 @@ struct SampleArgs {
 
 constexpr int kBins = 2592;       // bins of 1/64 octave of weight: 40.5 octaves, a multiple of 8 shares
 constexpr int kList = 512;        // candidates that one CTA ranks, one per thread
-constexpr int kMargin = 64;       // logits on both sides of the bin in which top-p's border is expected
+constexpr int kMargin = 64;       // logits on the far side of the bin in which top-p's border is expected
 constexpr int kTries = 2;         // guesses of the top-p border before the bisection
 constexpr int kSlots = kWarps * kClusterMax;
 constexpr int kPublished = 512;
@@ -335,6 +335,18 @@ __device__ __forceinline__ int rank_of(const u64* list, const u64* weight, int n
   return above;
 }
 
+// The weight of the candidates of list[0..n) whose key is at least `key`.
+__device__ __forceinline__ u64 weight_reaching(const u64* list, const u64* weight, int n, int per, uint32_t key) {
+  u64 w = 0;
+  for (int j = 2 * ((int)threadIdx.x & (per - 1)); j < n; j += 2 * per) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j);
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(weight + j);
+    w += ((uint32_t)(o.x >> 32) >= key ? v.x : 0) + ((uint32_t)(o.y >> 32) >= key ? v.y : 0);
+  }
+  for (int o = per >> 1; o > 0; o >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+  return w;
+}
+
 // The k-th largest of keys[0..n) (n a multiple of 16, k <= n) into *out.
 __device__ __forceinline__ void kth_key(const uint32_t* keys, int n, int k, uint32_t* out) {
   const int per = threads_per(n);
@@ -359,11 +371,12 @@ __device__ __forceinline__ void kth_key(const uint32_t* keys, int n, int k, uint
 constexpr int kCountBits = 23;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
 // Estimated weight of a bin, in units of the weight of the largest logit's
-// grid point: within a bin the weight falls by 1 - 2^(-1/64) = 0.010772.
+// grid point: a bin begins half a grid step above its first grid point, and
+// within it the weight falls by 1 - 2^(-1/64) = 0.010772.
 __device__ __forceinline__ float bin_estimate(uint32_t word, int bin) {
   const float c = (float)(word & kCountMask);
   const float places = c <= 32.f ? (float)(word >> kCountBits) : 7.5f * c;
-  return fast_exp2((float)bin * -0.015625f) * (c - (2.f * places + c) * (0.010772f / 32.f));
+  return fast_exp2((0.5f / kGrid) - (float)bin * 0.015625f) * (c - (2.f * places + c) * (0.010772f / 32.f));
 }
 // (logits, estimate) as one word of an exchange
 __device__ __forceinline__ u64 pack_est(uint32_t n, float e) { return ((u64)n << 32) | __float_as_uint(e); }
@@ -647,6 +660,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (min_p > 0.f) theta = fmaxf(base, add_up(m, s.delta[0], s.delta[1]));
   }
   auto weight = [&](float x) { return fixed(weight_of(rw, s.table, x)); };
+  // No logit less than `d` grid steps below the largest is below this: two steps
+  // and the rounding of |t| < 2^13 further down.
+  auto least_of = [&](int d) {
+    const float t = (float)(top_grid - d - 2) * (1.f / kGrid);
+    const float x = (t - fabsf(t) * 0x1p-20f) / rw.ch;
+    return (x - fabsf(x) * 0x1p-20f) + (rw.base - fabsf(rw.base) * 0x1p-22f);
+  };
   auto collect = [&](float x, int i) {
     const int at = atomicAdd(&s.count, 1);
     if (at < kList) s.cand[at] = ((u64)key_of(x) << 32) | (uint32_t)(lo + i);
@@ -745,9 +765,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       __syncthreads();
       for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist[b] = 0;
       __syncthreads();
+      // CTA r sums share r of the bins (from the largest weights down), thread i
+      // of it `per` bins, so that the slots of a meeting are in bin order too
+      const int own = kBins / (int)cl.size;
+      const int per = (own + kThreads - 1) / kThreads;
+      constexpr int kPer = (kBins + kThreads - 1) / kThreads;
       // the histogram and, for top-p, the exact weight of all
-      u64 all[1] = {0};
-      sl.template own<kResident, 2>([&](const float(&x)[kN], int, int) {
+      u64 all = 0;
+      sl.template own<kResident, 8 / kN>([&](const float(&x)[kN], int, int) {
         int bin[kN];
         uint32_t one[kN];
 #pragma unroll
@@ -757,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           int k = grid_of(p, &grid);
           if (by_weight) {
             const u64 w = fixed(weight_of(rw, s.table, x[i], &k));
-            all[0] += x[i] >= base ? w : 0;
+            all += x[i] >= base ? w : 0;
           }
           const int d = top_grid - k;
           bin[i] = d >> 3;
@@ -768,13 +793,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           if (x[i] >= base) atomicAdd(s.hist + bin[i], one[i]);
       });
       cl.sync();
-      // CTA r adds up share r of the bins (from the largest weights down) and
-      // leaves the sums in its own histogram, where no other CTA reads in this
-      // phase; thread i holds `per` bins of it, so slots are in bin order too
-      const int own = kBins / (int)cl.size;
-      const int per = (own + kThreads - 1) / kThreads;
-      constexpr int kPer = (kBins + kThreads - 1) / kThreads;
-      u64 v[2] = {0, Cluster::warp_sum(all[0])};
+      // a share's sums stay in its CTA's own histogram, where no other CTA
+      // reads in this phase
+      u64 v[2] = {0, Cluster::warp_sum(all)};
       {
         uint32_t n = 0;
         float e = 0.f;
@@ -817,12 +838,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         need = max(share_of(share, Cluster::warp_sum(cl.four(shares[1]).sum())), 1ull);
       else if (n_all <= (uint32_t)top_k)
         continue;  // the support holds no more
-      // the border is where the running sum reaches the aim: exact for counts
+      // the border is where the running estimate (for top-k the running count,
+      // which is exact) reaches the aim
       float aim = by_weight ? fmaxf(top_p, 0.f) * e_all : 0.f;
       // what the bisection below searches: [low, high], `over` above it
       float low = base, high = m, border = -INFINITY;
       u64 over = 0;
-      bool found = false;
+      bool found = false, listed = false;  // listed: what is in it is in s.cand
       for (int attempt = 0; attempt < kTries && !found; ++attempt) {
         // the first slot, then the first of its bins, where the running sum reaches the aim
         const uint32_t up_n = __shfl_up_sync(0xFFFFFFFFu, lane_n, 1);
@@ -863,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const float e_first = e;
         int cross = -1, in_cross = 0;
         uint32_t cross_n = 0;
-        float cross_e = 0.f;
+        float cross_e = 0.f, cross_w = 0.f;
         int last = -1;  // if rounding keeps all of them below the aim: the last one in use
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -873,6 +895,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             cross = owner * own + first + i;
             cross_n = n;
             cross_e = e;
+            cross_w = est[i];
             in_cross = (int)c;
           }
           n += c;
@@ -902,135 +925,144 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l0);
         cross_e = __shfl_sync(0xFFFFFFFFu, cross_e, l0);
         in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l0);
-        const bool heavy = in_cross > kList;
-        // the window: for top-p some logits of the bins on both sides
-        const uint32_t margin = by_weight && !heavy ? (uint32_t)min(kMargin, (kList - in_cross) / 2) : 0;
-        int b0 = cross, b1 = cross;
-        float e_b0 = cross_e;  // the estimate before the window
-        n = n_first;
-        e = e_first;
+        // The window of grid steps [c0, c1] in which the border is looked up: for
+        // top-k the bin; for top-p, in a bin of few logits, the bins around it
+        // with kMargin logits on both sides, in a bin of many the steps around
+        // the place in it where the estimate puts the border.
+        int c0 = 8 * cross, c1 = 8 * cross + 7;
+        float e_c0 = cross_e;  // the estimate before the window
+        if (by_weight && in_cross > kMargin) {
+          const float est_cross = __shfl_sync(0xFFFFFFFFu, cross_w, l0);
+          const float place = fminf(fmaxf((aim - cross_e) / est_cross, 0.f), 1.f) * 8.f;
+          const float reach = 8.f * kMargin / (float)in_cross + 1.f;
+          c0 += (int)floorf(place - reach);
+          c1 = 8 * cross + (int)ceilf(place + reach);
+          e_c0 += est_cross * (float)(c0 - 8 * cross) * 0.125f;
+        } else if (by_weight) {
+          n = n_first;
+          e = e_first;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int bin = owner * own + first + i;
-          const uint32_t c = word[i] & kCountMask;
-          if (margin > 0 && i < per && first + i < own) {
-            if (bin < cross && cross_n - n <= margin) {
-              b0 = min(b0, bin);
-              e_b0 = fminf(e_b0, e);
+          for (int i = 0; i < kPer; ++i) {
+            const int bin = owner * own + first + i;
+            const uint32_t c = word[i] & kCountMask;
+            if (i < per && first + i < own) {
+              if (bin < cross && cross_n - n <= kMargin) {
+                c0 = min(c0, 8 * bin);
+                e_c0 = fminf(e_c0, e);
+              }
+              if (bin > cross && n + c <= cross_n + in_cross + kMargin) c1 = max(c1, 8 * bin + 7);
             }
-            if (bin > cross && n + c <= cross_n + in_cross + margin) b1 = max(b1, bin);
+            n += c;
+            e += est[i];
           }
-          n += c;
-          e += est[i];
-        }
-        b0 = __reduce_min_sync(0xFFFFFFFFu, b0);
-        b1 = __reduce_max_sync(0xFFFFFFFFu, b1);
+          c0 = __reduce_min_sync(0xFFFFFFFFu, c0);
+          c1 = __reduce_max_sync(0xFFFFFFFFu, c1);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) e_b0 = fminf(e_b0, __shfl_xor_sync(0xFFFFFFFFu, e_b0, o));
-        // Every logit of the bins up to b1 is above `floor`: the bin's lower
-        // edge, two grid steps and the rounding of |t| < 2^13 further down.
-        const float floor_t = (float)(top_grid - 8 * (b1 + 1) - 2) * (1.f / kGrid);
-        const float floor = (floor_t - fabsf(floor_t) * 0x1p-20f) / rw.ch;
-        const float edge = fmaxf(base, (floor - fabsf(floor) * 0x1p-20f) + (rw.base - fabsf(rw.base) * 0x1p-22f));
+          for (int o = 16; o > 0; o >>= 1) e_c0 = fminf(e_c0, __shfl_xor_sync(0xFFFFFFFFu, e_c0, o));
+        }
+        const float edge = fmaxf(base, least_of(c1 + 1));
 
         // the exact weight above the window, and what is in the window
         if (threadIdx.x == 0) s.count = 0;
         __syncthreads();
-        u64 sums[2] = {0, 0};  // above the window, logits in it
+        u64 sums[3] = {0, 0, 0};  // weight above the window; logits and weight in it
         uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
-        const unsigned width = (unsigned)(b1 - b0);
+        const unsigned width = (unsigned)(c1 - c0);
         reaching(edge, [&](const float(&x)[kN], int i0) {
-          int b[kN];
+          int d[kN];
+          u64 w[kN];
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
             int k;
+            w[i] = 1;
             if (by_weight) {
-              const u64 w = fixed(weight_of(rw, s.table, x[i], &k));
-              b[i] = (top_grid - k) >> 3;
-              sums[0] += b[i] < b0 && x[i] >= base ? w : 0;
+              w[i] = fixed(weight_of(rw, s.table, x[i], &k));
+              sums[0] += x[i] >= base && top_grid - k < c0 ? w[i] : 0;
             } else {
               float grid;
-              b[i] = (top_grid - grid_of(fmaxf((x[i] - rw.base) * rw.ch, kLowest), &grid)) >> 3;
+              k = grid_of(fmaxf((x[i] - rw.base) * rw.ch, kLowest), &grid);
             }
-            if (!(x[i] >= base)) b[i] = -1;
+            d[i] = top_grid - k - c0;
           }
 #pragma unroll
           for (int i = 0; i < kN; ++i)
-            if (b[i] >= 0 && (unsigned)(b[i] - b0) <= width) {
+            if ((unsigned)d[i] <= width && x[i] >= base) {
               ++sums[1];
-              if (heavy) {
-                key_min = min(key_min, key_of(x[i]));
-                key_max = max(key_max, key_of(x[i]));
-              } else {
-                collect(x[i], i0 + i);
-              }
+              sums[2] += w[i];
+              const uint32_t key = key_of(x[i]);
+              key_min = min(key_min, key);
+              key_max = max(key_max, key);
+              collect(x[i], i0 + i);
             }
         });
-        if (heavy) {
-          key_max = cl.max(key_max);
-          key_min = ~cl.max(~key_min);
-        }
         const u64(*const met)[kSlots] = cl.sum(sums);
         over = by_weight ? sums[0] : cross_n;
-        if (heavy) {
-          // is it in the bin?  [low, high] covers the bin's logits, and no others
-          low = key_float(key_min);
-          high = key_float(key_max);
-          u64 in_bin[1] = {0};
-          reaching(low, [&](const float(&x)[kN], int) {
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (x[i] >= low && x[i] <= high) in_bin[0] += by_weight ? weight(x[i]) : 1;
-          });
-          cl.sum(in_bin);
-          if (over >= need || over + in_bin[0] < need) {
-            low = base;
-            high = m;
-            over = 0;
-          }
-          break;
-        }
-        const int n_list = (int)sums[1];
-        bring(met[1], n_list, !by_weight);
-        const int group = threads_per(n_list), i = (int)threadIdx.x / group;
-        const u64 c = s.list[i];
-        u64 upto;
-        rank_of(s.list, s.weight, n_list, group, c, &upto);
-        upto += over;
-        if (threadIdx.x == 0) s.found = 0;
-        __syncthreads();
-        if (c && over < need && upto >= need && upto - s.weight[i] < need) s.found = (uint32_t)(c >> 32);
-        __syncthreads();
-        if (s.found != 0) {
+        const bool inside = over < need && need <= over + sums[2];
+        if (inside && sums[1] <= kList) {
+          const int n_list = (int)sums[1];
+          bring(met[1], n_list, !by_weight);
+          const int group = threads_per(n_list), i = (int)threadIdx.x / group;
+          const uint32_t key = (uint32_t)(s.list[i] >> 32);  // 0 behind the last
+          if (threadIdx.x == 0) s.found = 0;
+          __syncthreads();
+          // the largest key whose equals and betters hold what is needed
+          if (over + weight_reaching(s.list, s.weight, n_list, group, key) >= need) atomicMax(&s.found, key);
+          __syncthreads();
           border = key_float(s.found);
           found = true;
+        } else if (inside) {
+          // many equal ones, or a bin far from even: [low, high] covers what is
+          // in the window, and no others
+          low = key_float(~cl.max(~key_min));
+          high = key_float(cl.max(key_max));
+          listed = cl.max((uint32_t)s.count) <= (uint32_t)kList;
+          break;
         } else {
           // the exact sums say by how much the estimate was off
           const float unit = (float)fixed(Weight{s.table[top_grid & (kGrid - 1)], rw.top - (top_grid >> kGridBits)});
-          aim = fmaxf(e_b0 + (float)(long long)(need - over) / unit, 0.f);
-          low = base;
-          high = m;
+          aim = fmaxf(e_c0 + (float)(long long)(need - over) / unit, 0.f);
           over = 0;
-          cl.sync();  // nobody reads the candidates any more
         }
       }
       if (!found) {
-        // the largest key whose logits, up to `high`, reach what is needed; `low` does
+        // the largest key whose logits, up to `high`, reach what is needed (`low`
+        // does), by quartering
         uint32_t from = key_of(low), to = key_of(high);
         while (from < to) {
-          const uint32_t mid = from + (to - from) / 2 + 1;
-          const float vmid = key_float(mid);
-          u64 c[1] = {0};
-          reaching(vmid, [&](const float(&x)[kN], int) {
+          const uint32_t span = to - from;
+          const uint32_t mid[3] = {from + span / 4 + 1, from + span / 2 + 1, from + span / 4 * 3 + 1};
+          u64 c[3] = {0, 0, 0};
+          if (listed) {
+            for (int i = threadIdx.x; i < s.count; i += kThreads) {
+              const uint32_t key = (uint32_t)(s.cand[i] >> 32);
+              const u64 w = by_weight ? weight(key_float(key)) : 1;
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (x[i] >= vmid && x[i] <= high) c[0] += by_weight ? weight(x[i]) : 1;
-          });
+              for (int j = 0; j < 3; ++j) c[j] += key >= mid[j] ? w : 0;
+            }
+            __syncwarp();
+          } else {
+            reaching(key_float(mid[0]), [&](const float(&x)[kN], int) {
+#pragma unroll
+              for (int i = 0; i < kN; ++i)
+                if (x[i] >= key_float(mid[0]) && x[i] <= high) {
+                  const u64 w = by_weight ? weight(x[i]) : 1;
+#pragma unroll
+                  for (int j = 0; j < 3; ++j) c[j] += x[i] >= key_float(mid[j]) ? w : 0;
+                }
+            });
+          }
           cl.sum(c);
-          if (over + c[0] >= need)
-            from = mid;
-          else
-            to = mid - 1;
+          if (over + c[2] >= need) {
+            from = mid[2];
+          } else if (over + c[1] >= need) {
+            from = mid[1];
+            to = mid[2] - 1;
+          } else if (over + c[0] >= need) {
+            from = mid[0];
+            to = mid[1] - 1;
+          } else {
+            to = mid[0] - 1;
+          }
         }
         border = key_float(from);
       }
