@@ -22,25 +22,32 @@
 // integers and 2^g - 1, |g| <= 1/1024, from two Taylor terms (the table
 // method of Tang 1989; the third term is below 2^-34).
 //
-// One thread-block cluster per row; each CTA keeps its slice of the row in
-// shared memory, so the logits cross HBM once whatever the filters need, and
-// the CTAs meet in distributed shared memory.  How the thresholds are found:
+// One thread-block cluster per row.  With few rows a row has up to eight CTAs,
+// each with its slice in shared memory, so that the logits cross HBM once
+// whatever the filters need; with many rows it has one, which reads again (from
+// L2, mostly) what little it needs again.  The CTAs meet in distributed shared
+// memory.  How the thresholds are found:
 //  * A small top-k (the usual one): every warp publishes its largest logits;
 //    the k-th largest of those bounds the k-th largest of the row from below
 //    and leaves about 1.4 k candidates, which one CTA ranks; top-p, min-p and
 //    the draw then look at the candidates alone.
 //  * A large top-k, or top-p over the whole vocabulary: a histogram of counts
-//    over 1/64 octaves of weight.  Counts place the k-th logit exactly; for
-//    top-p they place the border to within a few bins, then one pass sums the
-//    weight above those bins and the whole weight exactly and collects what is
-//    inside, which one CTA ranks.
-//  * Where a bin holds too many (ties): bisection over the logits' bits.
-#include <atomic>
+//    over 1/64 octaves of weight.  Counts place the k-th logit's bin exactly;
+//    for top-p they place the border to within a fraction of a bin.  One more
+//    pass sums the weight above a window around it exactly and collects what
+//    is inside, whose weights every CTA then adds up.
+//  * Where the window holds too many (ties): quartering of the logits' bits.
+// What bounds it: with many rows HBM (512 rows of 163840 fp32 logits under a
+// min-p: FIG_BATCH us, FIG_BATCHBW TB/s), or under top-p instruction issue (about 45
+// instructions a logit, 32 of them its weight); with few rows the latency of
+// the meetings (one row under top-k 50, top-p 0.9: FIG_ONE us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "sv_cluster.cuh"
 #include "sv_ptx.cuh"
@@ -54,10 +61,20 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 static_assert(kThreads == 512, "a thread per table entry and per candidate");
 constexpr int kClusterMax = 8;
-constexpr int kSupportBits = 40;     // weights below 2^-40 of the largest are left out
-constexpr int kMaxVocab = 1 << 22;   // leaves a weight 41 bits
-constexpr float kHottest = 1.2676506e30f;  // 2^100: beyond, 1/temperature loses bits
-constexpr float kCoarseMax = 4096.f;  // |x| log2(e)/temperature up to which the row needs no shift
+constexpr int kSlots = kWarps * kClusterMax;
+constexpr int kSupportBits = 40;            // weights below 2^-40 of the largest are left out
+constexpr int kMaxVocab = 1 << 22;          // leaves a weight 41 bits
+constexpr float kColdest = 5.4210109e-20f;  // 2^-64: temperatures below count as 0
+constexpr float kHottest = 1.2676506e30f;   // 2^100: beyond, 1/temperature loses bits
+constexpr float kCoarseMax = 4096.f;        // |x| log2(e)/temperature up to which the row needs no shift
+
+constexpr int kPieces = 4;       // bulk copies of a slice
+constexpr int kHold = 4;         // groups a thread holds when the token is looked up
+constexpr int kPublished = 512;  // largest logits published for a small top-k
+constexpr int kList = 512;       // candidates that one CTA ranks, one per thread
+constexpr int kBins = 2592;      // bins of 1/64 octave of weight: 40.5 octaves, a multiple of 8 shares
+constexpr int kMargin = 64;      // logits on both sides of the place where top-p's border is expected
+constexpr int kTries = 2;        // guesses of it before the quartering
 
 // round(2^31 2^(j/512)), j = 0..511, by the exponential series.
 constexpr int kGrid = 512, kGridBits = 9;
@@ -121,77 +138,68 @@ struct SampleArgs {
   int top_k_all;
   double ln_min_p_all;  // ln(min_p_all), 0 above 1
   long long row_stride;
-  int V, slice;  // slice: logits per CTA, a multiple of 8
-  int rows, ahead;  // row t + ahead is fetched into L2 early (0: none)
-  int down;      // the largest weight is mant << 31 >> down (mant < 2^32): V of them stay below 2^63
+  int V, slice;      // slice: logits per CTA, a multiple of 8
+  int rows, ahead;   // row t + ahead is fetched into L2 early (0: none)
+  int down;          // the largest weight is mant << 31 >> down (mant < 2^32): V of them stay below 2^63
   int32_t* tokens;
   float* probs;
   int32_t* status;
 };
 
-constexpr int kBins = 2592;       // bins of 1/64 octave of weight: 40.5 octaves, a multiple of 8 shares
-constexpr int kList = 512;        // candidates that one CTA ranks, one per thread
-constexpr int kMargin = 64;       // logits on the far side of the bin in which top-p's border is expected
-constexpr int kTries = 2;         // guesses of the top-p border before the bisection
-constexpr int kSlots = kWarps * kClusterMax;
-constexpr int kPublished = 512;
-constexpr int kPieces = 4;        // bulk copies of a slice
-constexpr int kHold = 4;          // groups a thread holds when the token is looked up
-
+// Shared memory of every row, and of rows with top-k or top-p.
 struct Shared {
   uint32_t table[kGrid];
-  __align__(16) u64 slot[2][3][kSlots];    // exchange: parity, value, (rank, warp)
+  __align__(16) u64 slot[2][3][kSlots];  // meetings: parity, value, (rank, warp)
+  u64 scan[kWarps];
+  u64 bar[kPieces];                      // arrival of the slice's pieces
+  float delta[2];
+  float inv_total;
+  int token;
+};
+struct Lists {
   __align__(16) uint32_t pub[kPublished];  // largest keys of every warp of the cluster
   __align__(16) u64 cand[kList];           // candidates of this CTA: key << 32 | index
   __align__(16) u64 list[kList];           // candidates of the cluster
   __align__(16) u64 weight[kList];         // their weights
   uint32_t hist[kBins];                    // see bin_estimate
-  u64 bar[kPieces];                        // arrival of the slice's pieces
   u64 sums[2];
   int count;                               // candidates found here
-  int token;
   uint32_t found;                          // a key
-  float delta[2];
 };
 
 // The weight function of a row, 2^((x - base) c).
 struct RowWeight {
   float base, ch, cl;  // c = ch + cl
+  float least;         // the support's end: smaller logits are taken for it
   int top;             // exponent of the largest weight, + down
 };
 struct Weight {
   uint32_t mant;  // [2^31, 2^32)
   int shift;      // the weight is (mant << 31) >> shift
 };
-__device__ __forceinline__ int grid_of(float p, float* grid) {
-  // p rounded to a multiple of 1/512: adding 1.5 * 2^14 leaves 9 fraction bits
-  const float k = p + 24576.f;
-  *grid = k - 24576.f;
+// t of a logit as k/512 + *g: adding 1.5 * 2^14 rounds it to 9 fraction bits.
+__device__ __forceinline__ int grid_of(const RowWeight& rw, float x, float* g) {
+  const float d = fmaxf(x, rw.least) - rw.base;  // (NaN: least)
+  const float k = fmaf(d, rw.ch, 24576.f);
+  *g = fmaf(d, rw.cl, fmaf(d, rw.ch, 24576.f - k));
   return (int)(__float_as_uint(k) - __float_as_uint(24576.f));
 }
-constexpr float kLowest = -7000.f;  // in place of every t far below those that count, -inf and NaN
-__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x, int* at) {
-  const float d = x - rw.base;
-  const float p = d * rw.ch;
-  const float e = fmaf(d, rw.cl, fmaf(d, rw.ch, -p));
-  const float pc = fmaxf(p, kLowest);
-  float grid;
-  const int k = grid_of(pc, &grid);
-  *at = k;
-  const float g = (pc - grid) + e;
-  const float r = g * fmaf(g, 0.2402265070f, 0.6931471806f);  // 2^g - 1
+__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x, int* at, float* g) {
+  const int k = *at = grid_of(rw, x, g);
+  const float r = *g * fmaf(*g, 0.2402265070f, 0.6931471806f);  // 2^g - 1
   Weight w;
   const uint32_t t = table[k & (kGrid - 1)];
   // t r, rounded to an integer by adding 1.5 * 2^23 (|t r| < 2^22); t as fp32
   // by its bits: 2^31 <= t < 2^32
   const float tf = __uint_as_float((t >> 8) + 0x4E800000u);
   w.mant = t + (__float_as_uint(fmaf(tf, r, 12582912.f)) - 0x4B400000u);
-  w.shift = min(rw.top - (k >> kGridBits), 63);
+  w.shift = rw.top - (k >> kGridBits);  // at most down + 41 <= 63
   return w;
 }
 __device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x) {
   int at;
-  return weight_of(rw, table, x, &at);
+  float g;
+  return weight_of(rw, table, x, &at, &g);
 }
 // The lowest bit is always set: like a rounding, unlike the cut alone, that
 // is right on average, so the sum of many small weights does not drift.
@@ -460,12 +468,17 @@ __device__ __forceinline__ float add_up(float m, float hi, float lo) {
 
 // Bounded wait for a piece (it is filled once).  Where it gives up the row's
 // results mean nothing, but every CTA still takes the same path: all that
-// decides it is exchanged first.
+// decides it is exchanged first.  After that it waits as long again, so that no
+// CTA ends with a copy into its shared memory under way.
 __device__ __forceinline__ bool wait_piece(uint32_t bar) {
   if (mbar_test(bar, 0)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_test(bar, 0))
-    if (globaltimer_ns() - t0 >= kWaitTimeoutNs) return false;
+    if (globaltimer_ns() - t0 >= kWaitTimeoutNs) {
+      while (!mbar_test(bar, 0) && globaltimer_ns() - t0 < 2 * kWaitTimeoutNs) {
+      }
+      return false;
+    }
   return true;
 }
 
@@ -475,88 +488,83 @@ __device__ __forceinline__ void prefetch_row(const Slice<T>& sl, long long away)
   const uintptr_t p = reinterpret_cast<uintptr_t>(sl.src + away);
   const uintptr_t p0 = (p + 15) & ~(uintptr_t)15, p1 = (p + (size_t)sl.n * sizeof(T)) & ~(uintptr_t)15;
   constexpr uintptr_t kPart = 16384;
-  const uintptr_t at = p0 + threadIdx.x * kPart;
-  if (at < p1)
+  for (uintptr_t at = p0 + threadIdx.x * kPart; at < p1; at += kThreads * kPart)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"((uint32_t)min(kPart, p1 - at)) : "memory");
 }
 
+// ---------------------------------------------------------------------------
+// A row, as one thread of its cluster sees it
+// ---------------------------------------------------------------------------
 template <typename T, bool kResident>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
-  extern __shared__ __align__(16) uint4 s_stage[];
-  __shared__ Shared s;
-  constexpr int kN = Vec<T>::kN;
-  Cluster cl{&s, cluster_rank(), cluster_size(), 0};
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first exchange
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = (int)(blockIdx.x / cl.size);
-  const long long lo = (long long)cl.rank * a.slice;
+struct Row {
+  using V = Vec<T>;
+  static constexpr int kN = V::kN;
+  static constexpr bool kInShared = kResident;
+  Cluster cl;
   Slice<T> sl;
-  sl.src = static_cast<const T*>(a.logits) + t * a.row_stride + lo;
-  sl.stage = s_stage;
-  sl.n = (int)max(0ll, min((long long)a.slice, a.V - lo));
-  sl.head = (int)((reinterpret_cast<uintptr_t>(sl.src) & 15u) / sizeof(T));
-  sl.groups = sl.n > 0 ? (sl.head + sl.n + kN - 1) / kN : 0;
+  RowWeight rw;
+  Shared* s;
+  int lo;          // index of the slice's first logit
+  float m;         // the largest logit
+  int top_grid;    // its place on the grid
+  // The thread's largest logit, its group, and the largest of the other groups:
+  // what is kept in the end is mostly a few logits, so that hardly a thread has
+  // to look at its logits again.
+  float top_here, next_here;
+  int top_group;
 
-  // the row's settings
-  const float u = __ldg(a.uniforms + t);
-  float tau = a.temperature ? __ldg(a.temperature + t) : a.temperature_all;
-  float top_p = a.top_p ? __ldg(a.top_p + t) : a.top_p_all;
-  float min_p = a.min_p ? __ldg(a.min_p + t) : a.min_p_all;
-  int top_k = a.top_k ? __ldg(a.top_k + t) : a.top_k_all;
-
-  // The slice comes in by bulk copies, one per piece, each with a barrier of
-  // its own, all started at once; the groups at its ends that reach beyond it
-  // are put together by threads.
-  const int inner0 = sl.head > 0 ? 1 : 0;
-  const int inner1 = sl.groups > 0 ? (sl.head + sl.n) / kN : 0;  // whole groups [inner0, inner1)
-  const int piece = (sl.groups + kPieces - 1) / kPieces;
-  if (kResident && threadIdx.x == 0) {
-    for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&s.bar[i]), 1);
-    fence_mbar_init_cluster();
-    for (int i = 0; i < kPieces; ++i) {
-      const int g0 = max(inner0, i * piece), g1 = min(inner1, (i + 1) * piece);
-      const uint32_t bar = smem_u32(&s.bar[i]);
-      if (g0 < g1) {
-        mbar_arrive_expect_tx(bar, (uint32_t)(g1 - g0) * 16u);
-        bulk_load(smem_u32(s_stage + g0), sl.src + (g0 * kN - sl.head), (uint32_t)(g1 - g0) * 16u, bar);
-      } else {
-        mbar_arrive(bar);
+  // The slice into shared memory: one bulk copy per piece, each with a barrier
+  // of its own, all started at once; the groups at its ends that reach beyond
+  // it are put together by threads.  Waits for the pieces of the warp's run.
+  __device__ __forceinline__ bool stage() {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int inner0 = sl.head > 0 ? 1 : 0, inner1 = sl.groups > 0 ? (sl.head + sl.n) / kN : 0;  // whole groups
+    const int piece = max(1, (sl.groups + kPieces - 1) / kPieces);
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&s->bar[i]), 1);
+      fence_mbar_init_cluster();
+      for (int i = 0; i < kPieces; ++i) {
+        const int g0 = max(inner0, i * piece), g1 = min(inner1, (i + 1) * piece);
+        const uint32_t bar = smem_u32(&s->bar[i]);
+        if (g0 < g1) {
+          mbar_arrive_expect_tx(bar, (uint32_t)(g1 - g0) * 16u);
+          bulk_load(smem_u32(sl.stage + g0), sl.src + (g0 * kN - sl.head), (uint32_t)(g1 - g0) * 16u, bar);
+        } else {
+          mbar_arrive(bar);
+        }
       }
     }
-  }
-  s.table[threadIdx.x] = kExp2.v[threadIdx.x];
-  if (kResident) {
     if (warp == 1 && lane < 2 && sl.groups > 0) {
       const int g = lane == 0 ? 0 : sl.groups - 1;
-      if (g < inner0 || g >= inner1) s_stage[g] = sl.fetch(g);
+      if (g < inner0 || g >= inner1) sl.stage[g] = sl.fetch(g);
     }
     __syncthreads();
     bool ok = true;
-    const int w0 = warp * sl.run(), w1 = w0 + sl.run();  // the warp's groups
-    for (int i = w0 / max(piece, 1); i < kPieces && i * piece < w1; ++i) ok &= wait_piece(smem_u32(&s.bar[i]));
-    if (!ok && a.status) atomicOr(a.status, SV_DEV_TIMEOUT);
+    const int w0 = warp * sl.run(), w1 = w0 + sl.run();
+    for (int i = w0 / piece; i < kPieces && i * piece < w1; ++i) ok &= wait_piece(smem_u32(&s->bar[i]));
+    return ok;
   }
-  // The thread's largest logit, its group, and the largest of the other groups
-  // (fmaxf passes over NaN): what is kept in the end is mostly a few logits, so
-  // that hardly a thread has to look at its logits again.
-  float top_here = -INFINITY, next_here = -INFINITY;
-  int top_group = 0;
-  sl.template own<kResident, kResident ? 4 : 8>([&](const float(&x)[kN], int, int g) {
-    const float v = max_of(x);
-    next_here = fmaxf(next_here, fminf(v, top_here));
-    if (v > top_here) {
-      top_here = v;
-      top_group = g;
-    }
-  });
-  // Rows that are not on the GPU yet start on their way into L2 while this one
-  // is past its pass over the logits.
-  if (!kResident && a.ahead > 0 && t + a.ahead < a.rows) prefetch_row<T>(sl, a.ahead * a.row_stride);
 
-  // f(x[kN], logit of x[0]) for the groups of the warp that reach `least`, each
-  // in some lane of it.  Lanes with more than one such group are served by the
-  // whole warp, unless there are many.
-  auto reaching = [&](float least, auto f) {
+  // the thread's largest logits (fmaxf passes over NaN)
+  __device__ __forceinline__ void find_top() {
+    top_here = next_here = -INFINITY;
+    top_group = 0;
+    sl.template own<kResident, kResident ? 4 : 8>([&](const float(&x)[kN], int, int g) {
+      const float v = max_of(x);
+      next_here = fmaxf(next_here, fminf(v, top_here));
+      if (v > top_here) {
+        top_here = v;
+        top_group = g;
+      }
+    });
+  }
+
+  // f(x[kN], logit of the slice of x[0]) for the groups of the warp that reach
+  // `least`, each in some lane of it.  Lanes with more than one such group are
+  // served by the whole warp, unless there are many.
+  template <class F>
+  __device__ __forceinline__ void reaching(float least, F f) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool more = next_here >= least;
     const unsigned many = __ballot_sync(0xFFFFFFFFu, more);
     auto look = [&](const float(&x)[kN], int i0, int) {
@@ -576,104 +584,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
     __syncwarp();
-  };
-
-  const bool greedy = tau < 5.4210109e-20f;  // 2^-64
-  if (greedy) {
-    tau = 1.f;
-    top_k = 0;
-    top_p = 1.f;
-    min_p = 1.f;
-  }
-  if (top_k >= a.V) top_k = 0;
-  if (min_p > 0.f && threadIdx.x == 0) {
-    // the distance from m at which min-p cuts, as a pair
-    const double ln = min_p >= 1.f ? 0.0 : (a.min_p ? log((double)min_p) : a.ln_min_p_all);
-    const double d = (double)tau * fmax(ln, -kSupportBits * 0.69314718055994530942);
-    s.delta[0] = (float)d;
-    s.delta[1] = (float)(d - (double)(float)d);
-  }
-  if (threadIdx.x == 0) s.count = 0;
-
-  // A small top-k looks at the largest logits of every warp, at least twice as
-  // many as it asks for: the k-th of half of them bounds about 1.4 k logits.
-  int rounds = 0;
-  if (top_k > 0) {
-    rounds = 1;
-    while (rounds < 8 && cl.slots() * rounds < 2 * top_k) rounds *= 2;
-    if (cl.slots() * rounds < 2 * top_k || cl.slots() * rounds > kPublished) rounds = 0;
-  }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the cluster runs
-  float m, bound = -INFINITY;  // at least top_k logits reach the bound
-  if (rounds > 0) {
-    uint32_t key = key_of(top_here);
-    for (int i = 0; i < rounds; ++i) {
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key);
-      if (lane < (int)cl.size) cluster_st(cluster_map(&s.pub[cl.place() * rounds + i], lane), top);
-      const unsigned who = __ballot_sync(0xFFFFFFFFu, key == top);
-      if (lane == __ffs(who) - 1) key = 0;
-    }
-    cl.sync();
-    const int n = cl.slots() * rounds;
-    uint32_t top = 0;
-    for (int i = lane; i < n; i += 32) top = max(top, s.pub[i]);
-    m = key_float(__reduce_max_sync(0xFFFFFFFFu, top));
-    kth_key(s.pub, n, top_k, &s.found);
-    bound = key_float(s.found);
-  } else {
-    m = key_float(cl.max(key_of(top_here)));
-  }
-  float* const probs = a.probs ? a.probs + (long long)t * a.V + lo : nullptr;
-  if (!(fabsf(m) < INFINITY) || !(tau <= kHottest)) {
-    // nothing to draw from: no finite largest logit, or no temperature
-    if (probs)
-      for (int i = threadIdx.x; i < sl.n; i += kThreads) probs[i] = 0.f;
-    if (cl.rank == 0 && threadIdx.x == 0) {
-      a.tokens[t] = -1;
-      if (a.status) atomicOr(a.status, SV_DEV_BAD_LOGITS);
-    }
-    return;
   }
 
-  // t = x log2(e)/temperature as a pair; rows with large |t| are shifted by
-  // their largest logit (there x - m is exact wherever the weight counts:
-  // |x - m| is then below a hundredth of |m|)
-  RowWeight rw;
-  int top_grid;
-  {
+  // The weight function and the support, once m is known.
+  __device__ __forceinline__ void set_weight(float tau, int down) {
     // log2(e) = 1.44269502 + 1.92596299e-8
     rw.ch = __fdiv_rn(1.44269502f, tau);
     rw.cl = (fmaf(-rw.ch, tau, 1.44269502f) + 1.92596299e-8f) / tau;
+    // rows with large |t| are shifted by their largest logit (there x - m is
+    // exact wherever the weight counts: |x - m| is then below a hundredth of |m|)
     rw.base = fabsf(m * rw.ch) < kCoarseMax ? 0.f : m;
-    float grid;
-    top_grid = grid_of((m - rw.base) * rw.ch, &grid);
-    rw.top = (top_grid >> kGridBits) + a.down;
-  }
-  // the support ends 40 ln 2 temperatures below m
-  float base, theta;
-  {
     constexpr double kWidth = kSupportBits * 0.69314718055994530942;
     constexpr float kHi = (float)kWidth, kLo = (float)(kWidth - (double)kHi);
     const float hi = tau * kHi;
-    base = add_up(m, -hi, -(fmaf(tau, kHi, -hi) + tau * kLo));
-    theta = base;
-    if (min_p > 0.f) theta = fmaxf(base, add_up(m, s.delta[0], s.delta[1]));
+    rw.least = add_up(m, -hi, -(fmaf(tau, kHi, -hi) + tau * kLo));
+    float g;
+    top_grid = grid_of(rw, m, &g);
+    rw.top = (top_grid >> kGridBits) + down;
   }
-  auto weight = [&](float x) { return fixed(weight_of(rw, s.table, x)); };
-  // No logit less than `d` grid steps below the largest is below this: two steps
+  __device__ __forceinline__ u64 weight(float x) const { return fixed(weight_of(rw, s->table, x)); }
+  // No logit less than d grid steps below the largest is below this: two steps
   // and the rounding of |t| < 2^13 further down.
-  auto least_of = [&](int d) {
+  __device__ __forceinline__ float least_of(int d) const {
     const float t = (float)(top_grid - d - 2) * (1.f / kGrid);
     const float x = (t - fabsf(t) * 0x1p-20f) / rw.ch;
     return (x - fabsf(x) * 0x1p-20f) + (rw.base - fabsf(rw.base) * 0x1p-22f);
-  };
-  auto collect = [&](float x, int i) {
-    const int at = atomicAdd(&s.count, 1);
-    if (at < kList) s.cand[at] = ((u64)key_of(x) << 32) | (uint32_t)(lo + i);
-  };
-  // The cluster's candidates, n <= kList of them, into s.list, and their
-  // weights (1 for a count) into s.weight; counts: each warp's share.
-  auto bring = [&](const u64* counts, int n, bool as_count) {
+  }
+
+  __device__ __forceinline__ void collect(Lists& f, float x, int i) const {
+    const int at = atomicAdd(&f.count, 1);
+    if (at < kList) f.cand[at] = ((u64)key_of(x) << 32) | (uint32_t)(lo + i);
+  }
+  // The cluster's candidates, n <= kList of them, into f.list, and their
+  // weights (1 for a count) into f.weight; counts: each warp's share.
+  __device__ __forceinline__ void bring(Lists& f, const u64* counts, bool as_count) const {
     int of_cta = (int)cl.four(counts).sum();  // lanes 4r .. 4r+3 hold CTA r's warps
     of_cta += __shfl_xor_sync(0xFFFFFFFFu, of_cta, 1);
     of_cta += __shfl_xor_sync(0xFFFFFFFFu, of_cta, 2);
@@ -690,476 +634,642 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     u64 v = 0, w = 0;
     if (here) {
-      v = cluster_ld64(&s.cand[at], from);
+      v = cluster_ld64(&f.cand[at], from);
       w = as_count ? 1 : weight(key_float((uint32_t)(v >> 32)));
     }
-    s.list[threadIdx.x] = v;
-    s.weight[threadIdx.x] = w;
+    f.list[threadIdx.x] = v;
+    f.weight[threadIdx.x] = w;
     __syncthreads();
-  };
-  const u64 share = fraction64(top_p), chance = greedy ? 0 : fraction64(u);
-  u64 total = 0;
-
-  bool done = false;
-  if (bound > -INFINITY) {
-    // ---- small top-k: the candidates decide
-    u64 mine[1] = {0};
-    reaching(bound, [&](const float(&x)[kN], int i0) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (x[i] >= bound) {
-          collect(x[i], i0 + i);
-          ++mine[0];
-        }
-    });
-    const u64(*const counts)[kSlots] = cl.sum(mine);
-    const int n = (int)min(mine[0], (u64)kList + 1);
-    done = n <= kList;
-    if (done && (probs || cl.rank == 0)) {
-      bring(counts[0], n, false);
-      const int per = threads_per(n), i = (int)threadIdx.x / per;
-      const bool speaks = i < n && ((int)threadIdx.x & (per - 1)) == 0;
-      const u64 c = s.list[i];  // 0 behind the last
-      const float x = c ? key_float((uint32_t)(c >> 32)) : -INFINITY;
-      // its rank, and the weight down to it (what is outside the support has
-      // rounding dust for a weight, and comes last)
-      u64 upto;
-      const int above = rank_of(s.list, s.weight, n, per, c, &upto);
-      if (speaks && above == top_k - 1) s.found = (uint32_t)(c >> 32);
-      __syncthreads();
-      const float x_k = fmaxf(base, key_float(s.found));
-      theta = fmaxf(theta, x_k);
-      if (top_p < 1.f) {
-        const int in_k = __syncthreads_count(speaks && x >= x_k);
-        if (speaks && above == in_k - 1) s.sums[0] = upto;
-        __syncthreads();
-        const u64 need = max(share_of(share, s.sums[0]), 1ull);
-        if (speaks && above < in_k && upto >= need && upto - s.weight[i] < need) s.found = (uint32_t)(c >> 32);
-        __syncthreads();
-        theta = fmaxf(theta, key_float(s.found));
-      }
-      const bool keep = speaks && x >= theta;
-      const int kept = __syncthreads_count(keep);
-      if (keep && above == kept - 1) s.sums[1] = upto;
-      // the kept ones in the order of the vocabulary: weight up to each index
-      __syncthreads();
-      total = s.sums[1];
-      if (cl.rank == 0) {
-        const u64 target = min(__umul64hi(chance, total), total - 1);
-        u64 until = 0;
-        for (int j = (int)threadIdx.x & (per - 1); j < n; j += per) {
-          const u64 o = s.list[j];
-          if (key_float((uint32_t)(o >> 32)) >= theta && (uint32_t)o <= (uint32_t)c) until += s.weight[j];
-        }
-        for (int o = per >> 1; o > 0; o >>= 1) until += __shfl_xor_sync(0xFFFFFFFFu, until, o);
-        if (keep && until > target && until - s.weight[i] <= target) a.tokens[t] = (int)(uint32_t)c;
-      }
-    }
-    if (done) cl.sync();  // nobody reads another's candidates any more
   }
-  if (!done) {
-    // ---- thresholds over the whole row: top-k, then top-p of what it leaves
-    for (int kind = 0; kind < 2; ++kind) {
-      const bool by_weight = kind == 1;
-      if (by_weight ? !(top_p < 1.f) : top_k <= 0) continue;
-      __syncthreads();
-      for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist[b] = 0;
-      __syncthreads();
-      // CTA r sums share r of the bins (from the largest weights down), thread i
-      // of it `per` bins, so that the slots of a meeting are in bin order too
-      const int own = kBins / (int)cl.size;
-      const int per = (own + kThreads - 1) / kThreads;
-      constexpr int kPer = (kBins + kThreads - 1) / kThreads;
-      // the histogram and, for top-p, the exact weight of all
-      u64 all = 0;
-      sl.template own<kResident, 8 / kN>([&](const float(&x)[kN], int, int) {
-        int bin[kN];
-        uint32_t one[kN];
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const float p = fmaxf((x[i] - rw.base) * rw.ch, kLowest);
-          float grid;
-          int k = grid_of(p, &grid);
-          if (by_weight) {
-            const u64 w = fixed(weight_of(rw, s.table, x[i], &k));
-            all += x[i] >= base ? w : 0;
-          }
-          const int d = top_grid - k;
-          bin[i] = d >> 3;
-          one[i] = 1u + ((uint32_t)(((d & 7) << 1) + (p < grid ? 1 : 0)) << kCountBits);
-        }
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (x[i] >= base) atomicAdd(s.hist + bin[i], one[i]);
-      });
-      cl.sync();
-      // a share's sums stay in its CTA's own histogram, where no other CTA
-      // reads in this phase
-      u64 v[2] = {0, Cluster::warp_sum(all)};
-      {
-        uint32_t n = 0;
-        float e = 0.f;
-        for (int i = 0; i < per; ++i) {
-          const int in_share = (int)threadIdx.x * per + i;
-          if (in_share < own) {
-            const int bin = (int)cl.rank * own + in_share;
-            uint32_t c[kClusterMax];
-#pragma unroll
-            for (uint32_t r = 1; r < kClusterMax; ++r) c[r] = r < cl.size ? cluster_ld(s.hist + bin, cl.rank ^ r) : 0;
-            c[0] = s.hist[bin];
-#pragma unroll
-            for (uint32_t r = 1; r < kClusterMax; ++r) c[0] += c[r];
-            s.hist[bin] = c[0];
-            n += c[0] & kCountMask;
-            e += bin_estimate(c[0], bin);
-          }
-        }
-        n = __reduce_add_sync(0xFFFFFFFFu, n);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
-        v[0] = pack_est(n, e);
-      }
-      const u64(*const shares)[kSlots] = cl.leave(v);
-      // every warp finds the border's bins by itself
-      const Cluster::Four slot = cl.four(shares[0]);
-      uint32_t slot_n[4], lane_n = 0;
-      float slot_e[4], lane_e = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lane_n += slot_n[i] = (uint32_t)(slot.v[i] >> 32);
-        lane_e += slot_e[i] = __uint_as_float((uint32_t)slot.v[i]);
-      }
-      lane_n = scan_add(lane_n);
-      lane_e = scan_add(lane_e);
-      const uint32_t n_all = __shfl_sync(0xFFFFFFFFu, lane_n, 31);
-      const float e_all = __shfl_sync(0xFFFFFFFFu, lane_e, 31);
-      u64 need = (u64)top_k;
-      if (by_weight)
-        need = max(share_of(share, Cluster::warp_sum(cl.four(shares[1]).sum())), 1ull);
-      else if (n_all <= (uint32_t)top_k)
-        continue;  // the support holds no more
-      // the border is where the running estimate (for top-k the running count,
-      // which is exact) reaches the aim
-      float aim = by_weight ? fmaxf(top_p, 0.f) * e_all : 0.f;
-      // what the bisection below searches: [low, high], `over` above it
-      float low = base, high = m, border = -INFINITY;
-      u64 over = 0;
-      bool found = false, listed = false;  // listed: what is in it is in s.cand
-      for (int attempt = 0; attempt < kTries && !found; ++attempt) {
-        // the first slot, then the first of its bins, where the running sum reaches the aim
-        const uint32_t up_n = __shfl_up_sync(0xFFFFFFFFu, lane_n, 1);
-        const float up_e = __shfl_up_sync(0xFFFFFFFFu, lane_e, 1);
-        uint32_t n = lane > 0 ? up_n : 0;  // before slot 4 lane + q
-        float e = lane > 0 ? up_e : 0.f;
-        int q = -1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (q < 0) {
-            if (slot_n[i] > 0 && (by_weight ? e + slot_e[i] >= aim : n + slot_n[i] >= (uint32_t)top_k)) {
-              q = i;
-            } else {
-              n += slot_n[i];
-              e += slot_e[i];
-            }
-          }
-        unsigned who = __ballot_sync(0xFFFFFFFFu, q >= 0);
-        if (who == 0) break;  // (rounding, or a second guess) beyond the last logit
-        int l0 = __ffs(who) - 1;
-        const int at = 4 * l0 + __shfl_sync(0xFFFFFFFFu, q, l0);
-        n = __shfl_sync(0xFFFFFFFFu, n, l0);
-        e = __shfl_sync(0xFFFFFFFFu, e, l0);
-        const int owner = at / kWarps;
-        const int first = ((at % kWarps) * 32 + lane) * per;
-        uint32_t word[kPer], n_here = 0;
-        float est[kPer], e_here = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          word[i] = i < per && first + i < own ? cluster_ld(s.hist + owner * own + first + i, (uint32_t)owner) : 0;
-          est[i] = bin_estimate(word[i], owner * own + first + i);
-          n_here += word[i] & kCountMask;
-          e_here += est[i];
-        }
-        n += scan_add(n_here) - n_here;
-        e += scan_add(e_here) - e_here;
-        const uint32_t n_first = n;
-        const float e_first = e;
-        int cross = -1, in_cross = 0;
-        uint32_t cross_n = 0;
-        float cross_e = 0.f, cross_w = 0.f;
-        int last = -1;  // if rounding keeps all of them below the aim: the last one in use
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const uint32_t c = word[i] & kCountMask;
-          if (c) last = i;
-          if (cross < 0 && c && (by_weight ? e + est[i] >= aim : n + c >= (uint32_t)top_k)) {
-            cross = owner * own + first + i;
-            cross_n = n;
-            cross_e = e;
-            cross_w = est[i];
-            in_cross = (int)c;
-          }
-          n += c;
-          e += est[i];
-        }
-        who = __ballot_sync(0xFFFFFFFFu, cross >= 0);
-        if (who == 0) {
-          n = n_first;
-          e = e_first;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            if (i == last) {
-              cross = owner * own + first + i;
-              cross_n = n;
-              cross_e = e;
-              in_cross = (int)(word[i] & kCountMask);
-            }
-            n += word[i] & kCountMask;
-            e += est[i];
-          }
-          who = __ballot_sync(0xFFFFFFFFu, last >= 0);
-          l0 = 31 - __clz(who);
-        } else {
-          l0 = __ffs(who) - 1;
-        }
-        cross = __shfl_sync(0xFFFFFFFFu, cross, l0);
-        cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l0);
-        cross_e = __shfl_sync(0xFFFFFFFFu, cross_e, l0);
-        in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l0);
-        // The window of grid steps [c0, c1] in which the border is looked up: for
-        // top-k the bin; for top-p, in a bin of few logits, the bins around it
-        // with kMargin logits on both sides, in a bin of many the steps around
-        // the place in it where the estimate puts the border.
-        int c0 = 8 * cross, c1 = 8 * cross + 7;
-        float e_c0 = cross_e;  // the estimate before the window
-        if (by_weight && in_cross > kMargin) {
-          const float est_cross = __shfl_sync(0xFFFFFFFFu, cross_w, l0);
-          const float place = fminf(fmaxf((aim - cross_e) / est_cross, 0.f), 1.f) * 8.f;
-          const float reach = 8.f * kMargin / (float)in_cross + 1.f;
-          c0 += (int)floorf(place - reach);
-          c1 = 8 * cross + (int)ceilf(place + reach);
-          e_c0 += est_cross * (float)(c0 - 8 * cross) * 0.125f;
-        } else if (by_weight) {
-          n = n_first;
-          e = e_first;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int bin = owner * own + first + i;
-            const uint32_t c = word[i] & kCountMask;
-            if (i < per && first + i < own) {
-              if (bin < cross && cross_n - n <= kMargin) {
-                c0 = min(c0, 8 * bin);
-                e_c0 = fminf(e_c0, e);
-              }
-              if (bin > cross && n + c <= cross_n + in_cross + kMargin) c1 = max(c1, 8 * bin + 7);
-            }
-            n += c;
-            e += est[i];
-          }
-          c0 = __reduce_min_sync(0xFFFFFFFFu, c0);
-          c1 = __reduce_max_sync(0xFFFFFFFFu, c1);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) e_c0 = fminf(e_c0, __shfl_xor_sync(0xFFFFFFFFu, e_c0, o));
-        }
-        const float edge = fmaxf(base, least_of(c1 + 1));
+};
 
-        // the exact weight above the window, and what is in the window
-        if (threadIdx.x == 0) s.count = 0;
-        __syncthreads();
-        u64 sums[3] = {0, 0, 0};  // weight above the window; logits and weight in it
-        uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
-        const unsigned width = (unsigned)(c1 - c0);
-        reaching(edge, [&](const float(&x)[kN], int i0) {
-          int d[kN];
-          u64 w[kN];
+// ---------------------------------------------------------------------------
+// A small top-k: the candidates decide
+// ---------------------------------------------------------------------------
+// Warps' largest logits to publish for a top-k, at least twice as many in all as
+// it asks for (the k-th of half of them bounds about 1.4 k logits); 0: too many.
+__device__ __forceinline__ int publish_rounds(int top_k, int slots) {
+  if (top_k <= 0) return 0;
+  int rounds = 1;
+  while (rounds < 8 && slots * rounds < 2 * top_k) rounds *= 2;
+  return slots * rounds < 2 * top_k || slots * rounds > kPublished ? 0 : rounds;
+}
+
+// Every warp's `rounds` largest logits to every CTA: sets row.m, and returns a
+// bound that at least top_k logits of the row reach.
+template <class R>
+__device__ __forceinline__ float publish(R& row, Lists& f, int rounds, int top_k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key = key_of(row.top_here);
+  for (int i = 0; i < rounds; ++i) {
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, key);
+    if (lane < (int)row.cl.size) cluster_st(cluster_map(&f.pub[row.cl.place() * rounds + i], lane), top);
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, key == top);
+    if (lane == __ffs(who) - 1) key = 0;
+  }
+  row.cl.sync();
+  const int n = row.cl.slots() * rounds;
+  uint32_t top = 0;
+  for (int i = lane; i < n; i += 32) top = max(top, f.pub[i]);
+  row.m = key_float(__reduce_max_sync(0xFFFFFFFFu, top));
+  kth_key(f.pub, n, top_k, &f.found);
+  return key_float(f.found);
+}
+
+// False where the logits that reach the bound are too many.  Else, in the CTAs
+// that speak for the row, *theta and *total are set; rank 0 writes the token.
+template <class R>
+__device__ __forceinline__ bool small_top_k(R& row, Lists& f, const SampleArgs& a, int t, int top_k, float bound, float top_p,
+                                            u64 chance, float* theta, u64* total) {
+  constexpr int kN = R::kN;
+  u64 mine[1] = {0};
+  row.reaching(bound, [&](const float(&x)[kN], int i0) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            int k;
-            w[i] = 1;
-            if (by_weight) {
-              w[i] = fixed(weight_of(rw, s.table, x[i], &k));
-              sums[0] += x[i] >= base && top_grid - k < c0 ? w[i] : 0;
-            } else {
-              float grid;
-              k = grid_of(fmaxf((x[i] - rw.base) * rw.ch, kLowest), &grid);
-            }
-            d[i] = top_grid - k - c0;
-          }
+    for (int i = 0; i < kN; ++i)
+      if (x[i] >= bound) {
+        row.collect(f, x[i], i0 + i);
+        ++mine[0];
+      }
+  });
+  const u64(*const counts)[kSlots] = row.cl.sum(mine);
+  if (mine[0] > kList) return false;
+  const int n = (int)mine[0];
+  if (a.probs || row.cl.rank == 0) {
+    row.bring(f, counts[0], false);
+    const int per = threads_per(n), i = (int)threadIdx.x / per;
+    const bool speaks = i < n && ((int)threadIdx.x & (per - 1)) == 0;
+    const u64 c = f.list[i];  // 0 behind the last
+    const float x = c ? key_float((uint32_t)(c >> 32)) : -INFINITY;
+    // its rank, and the weight down to it (what is outside the support comes last)
+    u64 upto;
+    const int above = rank_of(f.list, f.weight, n, per, c, &upto);
+    if (speaks && above == top_k - 1) f.found = (uint32_t)(c >> 32);
+    __syncthreads();
+    const float x_k = fmaxf(row.rw.least, key_float(f.found));
+    float keep_from = fmaxf(*theta, x_k);
+    if (top_p < 1.f) {
+      const int in_k = __syncthreads_count(speaks && x >= x_k);
+      if (speaks && above == in_k - 1) f.sums[0] = upto;
+      __syncthreads();
+      const u64 need = max(share_of(fraction64(top_p), f.sums[0]), 1ull);
+      if (speaks && above < in_k && upto >= need && upto - f.weight[i] < need) f.found = (uint32_t)(c >> 32);
+      __syncthreads();
+      keep_from = fmaxf(keep_from, key_float(f.found));
+    }
+    const bool keep = speaks && x >= keep_from;
+    const int kept = __syncthreads_count(keep);
+    if (keep && above == kept - 1) f.sums[1] = upto;
+    __syncthreads();
+    *total = f.sums[1];
+    *theta = keep_from;
+    if (row.cl.rank == 0) {
+      // the kept ones in the order of the vocabulary: the weight up to each index
+      const u64 target = min(__umul64hi(chance, *total), *total - 1);
+      u64 until = 0;
+      for (int j = (int)threadIdx.x & (per - 1); j < n; j += per) {
+        const u64 o = f.list[j];
+        if (key_float((uint32_t)(o >> 32)) >= keep_from && (uint32_t)o <= (uint32_t)c) until += f.weight[j];
+      }
+      for (int o = per >> 1; o > 0; o >>= 1) until += __shfl_xor_sync(0xFFFFFFFFu, until, o);
+      if (keep && until > target && until - f.weight[i] <= target) a.tokens[t] = (int)(uint32_t)c;
+    }
+  }
+  row.cl.sync();  // nobody reads another's candidates any more
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// The threshold of top-k or top-p over the whole row
+// ---------------------------------------------------------------------------
+struct Border {
+  float x;     // the threshold; -inf where everything stays
+  bool ready;  // top-p: `here` is the thread's weight above the window, and f.cand holds what is in it
+  u64 here;
+};
+
+// kWeight false: the top_k-th largest of the logits >= base.  kWeight true: the
+// largest logit from which on the logits >= base hold the share top_p of their
+// weight.  base is inside the support.
+template <bool kWeight, class R>
+__device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int top_k, float top_p) {
+  constexpr int kN = R::kN;
+  constexpr bool kResident = R::kInShared;
+  Cluster& cl = row.cl;
+  const int lane = threadIdx.x & 31;
+  Border out{-INFINITY, false, 0};
+  __syncthreads();
+  for (int b = threadIdx.x; b < kBins; b += kThreads) f.hist[b] = 0;
+  __syncthreads();
+  // the histogram and, for top-p, the exact weight of all
+  u64 all = 0;
+  row.sl.template own<kResident, 8 / kN>([&](const float(&x)[kN], int, int) {
+    int bin[kN];
+    uint32_t one[kN];
 #pragma unroll
-          for (int i = 0; i < kN; ++i)
-            if ((unsigned)d[i] <= width && x[i] >= base) {
-              ++sums[1];
-              sums[2] += w[i];
-              const uint32_t key = key_of(x[i]);
-              key_min = min(key_min, key);
-              key_max = max(key_max, key);
-              collect(x[i], i0 + i);
-            }
-        });
-        const u64(*const met)[kSlots] = cl.sum(sums);
-        over = by_weight ? sums[0] : cross_n;
-        const bool inside = over < need && need <= over + sums[2];
-        if (inside && sums[1] <= kList) {
-          const int n_list = (int)sums[1];
-          bring(met[1], n_list, !by_weight);
-          const int group = threads_per(n_list), i = (int)threadIdx.x / group;
-          const uint32_t key = (uint32_t)(s.list[i] >> 32);  // 0 behind the last
-          if (threadIdx.x == 0) s.found = 0;
-          __syncthreads();
-          // the largest key whose equals and betters hold what is needed
-          if (over + weight_reaching(s.list, s.weight, n_list, group, key) >= need) atomicMax(&s.found, key);
-          __syncthreads();
-          border = key_float(s.found);
-          found = true;
-        } else if (inside) {
-          // many equal ones, or a bin far from even: [low, high] covers what is
-          // in the window, and no others
-          low = key_float(~cl.max(~key_min));
-          high = key_float(cl.max(key_max));
-          listed = cl.max((uint32_t)s.count) <= (uint32_t)kList;
-          break;
+    for (int i = 0; i < kN; ++i) {
+      int k;
+      float g;
+      if (kWeight) {
+        const u64 w = fixed(weight_of(row.rw, row.s->table, x[i], &k, &g));
+        all += x[i] >= base ? w : 0;
+      } else {
+        k = grid_of(row.rw, x[i], &g);
+      }
+      const int d = row.top_grid - k;
+      bin[i] = d >> 3;
+      one[i] = 1u + ((uint32_t)(((d & 7) << 1) + (int)(__float_as_uint(g) >> 31)) << kCountBits);
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (x[i] >= base) atomicAdd(f.hist + bin[i], one[i]);
+  });
+  cl.sync();
+  // CTA r adds up share r of the bins (from the largest weights down), thread i
+  // of it `per` bins, so that the slots of a meeting are in bin order too.  A
+  // share's sums stay in its CTA's own histogram, where no other CTA reads now.
+  const int own = kBins / (int)cl.size;
+  const int per = (own + kThreads - 1) / kThreads;
+  constexpr int kPer = (kBins + kThreads - 1) / kThreads;
+  u64 v[2] = {0, Cluster::warp_sum(all)};
+  {
+    uint32_t n = 0;
+    float e = 0.f;
+    for (int i = 0; i < per; ++i) {
+      const int in_share = (int)threadIdx.x * per + i;
+      if (in_share < own) {
+        const int bin = (int)cl.rank * own + in_share;
+        uint32_t c[kClusterMax];
+#pragma unroll
+        for (uint32_t r = 1; r < kClusterMax; ++r) c[r] = r < cl.size ? cluster_ld(f.hist + bin, cl.rank ^ r) : 0;
+        c[0] = f.hist[bin];
+#pragma unroll
+        for (uint32_t r = 1; r < kClusterMax; ++r) c[0] += c[r];
+        f.hist[bin] = c[0];
+        n += c[0] & kCountMask;
+        e += bin_estimate(c[0], bin);
+      }
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
+    v[0] = pack_est(n, e);
+  }
+  const u64(*const shares)[kSlots] = cl.leave(v);
+  // every warp finds the border's bin by itself
+  const Cluster::Four slot = cl.four(shares[0]);
+  uint32_t slot_n[4], lane_n = 0;
+  float slot_e[4], lane_e = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lane_n += slot_n[i] = (uint32_t)(slot.v[i] >> 32);
+    lane_e += slot_e[i] = __uint_as_float((uint32_t)slot.v[i]);
+  }
+  lane_n = scan_add(lane_n);
+  lane_e = scan_add(lane_e);
+  const uint32_t n_all = __shfl_sync(0xFFFFFFFFu, lane_n, 31);
+  const float e_all = __shfl_sync(0xFFFFFFFFu, lane_e, 31);
+  u64 need = (u64)top_k;
+  if (kWeight)
+    need = max(share_of(fraction64(top_p), Cluster::warp_sum(cl.four(shares[1]).sum())), 1ull);
+  else if (n_all <= (uint32_t)top_k)
+    return out;  // the support holds no more
+  // the border is where the running estimate (for top-k the running count,
+  // which is exact) reaches the aim
+  float aim = kWeight ? fmaxf(top_p, 0.f) * e_all : 0.f;
+  auto reached = [&](uint32_t n, float e) { return kWeight ? e >= aim : n >= (uint32_t)top_k; };
+  // what the quartering below searches: [low, high], `over` above it
+  float low = base, high = row.m;
+  u64 over = 0;
+  bool listed = false;  // what is in it is in f.cand
+  for (int attempt = 0; attempt < kTries; ++attempt) {
+    // the first slot, then the first of its bins, where the aim is reached
+    const uint32_t up_n = __shfl_up_sync(0xFFFFFFFFu, lane_n, 1);
+    const float up_e = __shfl_up_sync(0xFFFFFFFFu, lane_e, 1);
+    uint32_t n = lane > 0 ? up_n : 0;  // before slot 4 lane + q
+    float e = lane > 0 ? up_e : 0.f;
+    int q = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (q < 0) {
+        if (slot_n[i] > 0 && reached(n + slot_n[i], e + slot_e[i])) {
+          q = i;
         } else {
-          // the exact sums say by how much the estimate was off
-          const float unit = (float)fixed(Weight{s.table[top_grid & (kGrid - 1)], rw.top - (top_grid >> kGridBits)});
-          aim = fmaxf(e_c0 + (float)(long long)(need - over) / unit, 0.f);
-          over = 0;
+          n += slot_n[i];
+          e += slot_e[i];
         }
       }
-      if (!found) {
-        // the largest key whose logits, up to `high`, reach what is needed (`low`
-        // does), by quartering
-        uint32_t from = key_of(low), to = key_of(high);
-        while (from < to) {
-          const uint32_t span = to - from;
-          const uint32_t mid[3] = {from + span / 4 + 1, from + span / 2 + 1, from + span / 4 * 3 + 1};
-          u64 c[3] = {0, 0, 0};
-          if (listed) {
-            for (int i = threadIdx.x; i < s.count; i += kThreads) {
-              const uint32_t key = (uint32_t)(s.cand[i] >> 32);
-              const u64 w = by_weight ? weight(key_float(key)) : 1;
+    unsigned who = __ballot_sync(0xFFFFFFFFu, q >= 0);
+    if (who == 0) break;  // (rounding, or a second guess) beyond the last logit
+    int l0 = __ffs(who) - 1;
+    const int at = 4 * l0 + __shfl_sync(0xFFFFFFFFu, q, l0);
+    n = __shfl_sync(0xFFFFFFFFu, n, l0);
+    e = __shfl_sync(0xFFFFFFFFu, e, l0);
+    const int owner = at / kWarps;
+    const int first = ((at % kWarps) * 32 + lane) * per;  // the lane's bins of the slot, in its share
+    const int bin0 = owner * own + first;
+    uint32_t word[kPer], n_here = 0;
+    float est[kPer], e_here = 0.f;
 #pragma unroll
-              for (int j = 0; j < 3; ++j) c[j] += key >= mid[j] ? w : 0;
-            }
-            __syncwarp();
-          } else {
-            reaching(key_float(mid[0]), [&](const float(&x)[kN], int) {
+    for (int i = 0; i < kPer; ++i) {
+      word[i] = i < per && first + i < own ? cluster_ld(f.hist + bin0 + i, (uint32_t)owner) : 0;
+      est[i] = bin_estimate(word[i], bin0 + i);
+      n_here += word[i] & kCountMask;
+      e_here += est[i];
+    }
+    const uint32_t n_first = n + scan_add(n_here) - n_here;
+    const float e_first = e + (scan_add(e_here) - e_here);
+    // that bin: logits and weight before it, in it; where rounding keeps all of
+    // them below the aim, the last bin in use
+    int cross = -1, last = -1, in_cross = 0;
+    uint32_t cross_n = 0;
+    float cross_e = 0.f, cross_w = 0.f;
+    n = n_first;
+    e = e_first;
 #pragma unroll
-              for (int i = 0; i < kN; ++i)
-                if (x[i] >= key_float(mid[0]) && x[i] <= high) {
-                  const u64 w = by_weight ? weight(x[i]) : 1;
-#pragma unroll
-                  for (int j = 0; j < 3; ++j) c[j] += x[i] >= key_float(mid[j]) ? w : 0;
-                }
-            });
-          }
-          cl.sum(c);
-          if (over + c[2] >= need) {
-            from = mid[2];
-          } else if (over + c[1] >= need) {
-            from = mid[1];
-            to = mid[2] - 1;
-          } else if (over + c[0] >= need) {
-            from = mid[0];
-            to = mid[1] - 1;
-          } else {
-            to = mid[0] - 1;
-          }
-        }
-        border = key_float(from);
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t c = word[i] & kCountMask;
+      const bool take = c && cross < 0 && reached(n + c, e + est[i]);
+      if (take) cross = bin0 + i;
+      if (c && (take || cross < 0)) {
+        last = bin0 + i;
+        cross_n = n;
+        cross_e = e;
+        cross_w = est[i];
+        in_cross = (int)c;
       }
-      base = fmaxf(base, border);
-      theta = fmaxf(theta, border);
+      n += c;
+      e += est[i];
+    }
+    who = __ballot_sync(0xFFFFFFFFu, cross >= 0);
+    l0 = who ? __ffs(who) - 1 : 31 - __clz(__ballot_sync(0xFFFFFFFFu, last >= 0));
+    cross = __shfl_sync(0xFFFFFFFFu, last, l0);
+    cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l0);
+    cross_e = __shfl_sync(0xFFFFFFFFu, cross_e, l0);
+    cross_w = __shfl_sync(0xFFFFFFFFu, cross_w, l0);
+    in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l0);
+    // The window of grid steps [c0, c1] in which the border is looked up: for
+    // top-k the bin; for top-p, in a bin of few logits, the bins around it with
+    // kMargin logits on both sides, in a bin of many the steps around the place
+    // in it where the estimate puts the border.
+    int c0 = 8 * cross, c1 = 8 * cross + 7;
+    float e_c0 = cross_e;  // the estimate before the window
+    if (kWeight && in_cross > kMargin) {
+      const float place = fminf(fmaxf((aim - cross_e) / cross_w, 0.f), 1.f) * 8.f;
+      const float reach = 8.f * kMargin / (float)in_cross + 1.f;
+      c0 += (int)floorf(place - reach);
+      c1 = 8 * cross + (int)ceilf(place + reach);
+      e_c0 += cross_w * (float)(c0 - 8 * cross) * 0.125f;
+    } else if (kWeight) {
+      n = n_first;
+      e = e_first;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int bin = bin0 + i;
+        const uint32_t c = word[i] & kCountMask;
+        if (i < per && first + i < own) {
+          if (bin < cross && cross_n - n <= kMargin) {
+            c0 = min(c0, 8 * bin);
+            e_c0 = fminf(e_c0, e);
+          }
+          if (bin > cross && n + c <= cross_n + in_cross + kMargin) c1 = max(c1, 8 * bin + 7);
+        }
+        n += c;
+        e += est[i];
+      }
+      c0 = __reduce_min_sync(0xFFFFFFFFu, c0);
+      c1 = __reduce_max_sync(0xFFFFFFFFu, c1);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) e_c0 = fminf(e_c0, __shfl_xor_sync(0xFFFFFFFFu, e_c0, o));
     }
 
-    // ---- the draw, in the order of the vocabulary: the warp that holds the
-    // token, then its whole CTA looks at that warp's logits
-    u64 mine = 0;
-    reaching(theta, [&](const float(&x)[kN], int) {
+    // the exact weight above the window, and what is in the window
+    if (threadIdx.x == 0) f.count = 0;
+    __syncthreads();
+    u64 sums[3] = {0, 0, 0};  // weight above the window; logits and weight in it
+    uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
+    const unsigned width = (unsigned)(c1 - c0);
+    row.reaching(fmaxf(base, row.least_of(c1 + 1)), [&](const float(&x)[kN], int i0) {
+      int d[kN];
+      u64 w[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        const u64 w = weight(x[i]);
-        mine += x[i] >= theta ? w : 0;
+        int k;
+        float g;
+        w[i] = 1;
+        if (kWeight) {
+          w[i] = fixed(weight_of(row.rw, row.s->table, x[i], &k, &g));
+          sums[0] += x[i] >= base && row.top_grid - k < c0 ? w[i] : 0;
+        } else {
+          k = grid_of(row.rw, x[i], &g);
+        }
+        d[i] = row.top_grid - k - c0;
       }
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if ((unsigned)d[i] <= width && x[i] >= base) {
+          ++sums[1];
+          sums[2] += w[i];
+          const uint32_t key = key_of(x[i]);
+          key_min = min(key_min, key);
+          key_max = max(key_max, key);
+          row.collect(f, x[i], i0 + i);
+        }
     });
-    const u64 of_warp[1] = {Cluster::warp_sum(mine)};
-    const Cluster::Four f = cl.four(cl.leave(of_warp)[0]);
-    const u64 until = scan_add(f.sum());
-    total = __shfl_sync(0xFFFFFFFFu, until, 31);
-    const u64 target = min(__umul64hi(chance, total), total - 1);
-    int at = -1;
-    u64 before = until - f.sum();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (at < 0 && target >= before && target - before < f.v[i]) at = 4 * lane + i;
-      if (at < 0) before += f.v[i];
+    out.here = sums[0];
+    const u64(*const met)[kSlots] = cl.sum(sums);
+    over = kWeight ? sums[0] : cross_n;
+    const bool inside = over < need && need <= over + sums[2];
+    if (inside && sums[1] <= kList) {
+      const int n_list = (int)sums[1];
+      row.bring(f, met[1], !kWeight);
+      const int group = threads_per(n_list);
+      const uint32_t key = (uint32_t)(f.list[threadIdx.x / group] >> 32);  // 0 behind the last
+      if (threadIdx.x == 0) f.found = 0;
+      __syncthreads();
+      // the largest key whose equals and betters hold what is needed
+      if (over + weight_reaching(f.list, f.weight, n_list, group, key) >= need) atomicMax(&f.found, key);
+      __syncthreads();
+      out.x = key_float(f.found);
+      out.ready = kWeight;
+      return out;
     }
-    const int l0 = __ffs(__ballot_sync(0xFFFFFFFFu, at >= 0)) - 1;
-    at = __shfl_sync(0xFFFFFFFFu, at, l0);
-    before = __shfl_sync(0xFFFFFFFFu, before, l0);
-    if (at / kWarps == (int)cl.rank) {
-      const int end = min(sl.groups, (at % kWarps + 1) * sl.run());
-      for (int g0 = at % kWarps * sl.run(); g0 < end; g0 += kThreads * kHold) {
-        // a thread takes up to kHold neighbouring groups
-        const int hold = min(kHold, (end - g0 + kThreads - 1) / kThreads), first = g0 + (int)threadIdx.x * hold;
-        uint4 v[kHold];
-        u64 sum = 0;
+    if (inside) {
+      // many equal ones, or a bin far from even: [low, high] covers what is in
+      // the window, and no others
+      low = key_float(~cl.max(~key_min));
+      high = key_float(cl.max(key_max));
+      listed = cl.max((uint32_t)f.count) <= (uint32_t)kList;
+      break;
+    }
+    // the exact sums say by how much the estimate was off
+    const float unit = (float)fixed(Weight{row.s->table[row.top_grid & (kGrid - 1)], row.rw.top - (row.top_grid >> kGridBits)});
+    aim = fmaxf(e_c0 + (float)(long long)(need - over) / unit, 0.f);
+    over = 0;
+  }
+  // The largest key whose logits, up to `high`, hold what is needed (those of
+  // `low` do), by quartering.
+  uint32_t from = key_of(low), to = key_of(high);
+  while (from < to) {
+    const uint32_t span = to - from;
+    const uint32_t mid[3] = {from + span / 4 + 1, from + span / 2 + 1, from + span / 4 * 3 + 1};
+    u64 c[3] = {0, 0, 0};
+    if (listed) {
+      for (int i = threadIdx.x; i < f.count; i += kThreads) {
+        const uint32_t key = (uint32_t)(f.cand[i] >> 32);
+        const u64 w = kWeight ? row.weight(key_float(key)) : 1;
 #pragma unroll
-        for (int j = 0; j < kHold; ++j)
-          v[j] = j < hold && first + j < end ? sl.template raw<kResident>(first + j) : Slice<T>::nothing();
+        for (int j = 0; j < 3; ++j) c[j] += key >= mid[j] ? w : 0;
+      }
+      __syncwarp();
+    } else {
+      row.reaching(key_float(mid[0]), [&](const float(&x)[kN], int) {
 #pragma unroll
-        for (int j = 0; j < kHold; ++j) {
-          float x[kN];
-          Vec<T>::unpack(v[j], x);
-          if (max_of(x) >= theta) {
+        for (int i = 0; i < kN; ++i)
+          if (x[i] >= key_float(mid[0]) && x[i] <= high) {
+            const u64 w = kWeight ? row.weight(x[i]) : 1;
 #pragma unroll
-            for (int i = 0; i < kN; ++i) sum += x[i] >= theta ? weight(x[i]) : 0;
+            for (int j = 0; j < 3; ++j) c[j] += x[i] >= key_float(mid[j]) ? w : 0;
           }
-        }
-        u64 upto = scan_add(sum);
-        __syncthreads();
-        if (lane == 31) s.weight[warp] = upto;
-        __syncthreads();
-        u64 all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) upto += s.weight[w];
-          all += s.weight[w];
-        }
-        upto += before;
-        if (target >= upto - sum && target < upto) {
-          u64 c = upto - sum;
-          int token = -1;
+      });
+    }
+    cl.sum(c);
+    if (over + c[2] >= need) {
+      from = mid[2];
+    } else if (over + c[1] >= need) {
+      from = mid[1];
+      to = mid[2] - 1;
+    } else if (over + c[0] >= need) {
+      from = mid[0];
+      to = mid[1] - 1;
+    } else {
+      to = mid[0] - 1;
+    }
+  }
+  out.x = key_float(from);
+  return out;
+}
+
+// ---------------------------------------------------------------------------
+// The draw
+// ---------------------------------------------------------------------------
+// From the logits >= theta in the order of the vocabulary: the warp that holds
+// the token, then its whole CTA looks at that warp's logits.  mine: the thread's
+// share of its warp's weight.  Returns the total.
+template <class R>
+__device__ __forceinline__ u64 draw(R& row, const SampleArgs& a, int t, float theta, u64 mine, u64 chance, bool tell_all) {
+  constexpr int kN = R::kN;
+  constexpr bool kResident = R::kInShared;
+  Cluster& cl = row.cl;
+  const auto& sl = row.sl;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 of_warp[1] = {Cluster::warp_sum(mine)};
+  const Cluster::Four f = cl.four(cl.leave(of_warp)[0]);
+  const u64 until = scan_add(f.sum());
+  const u64 total = __shfl_sync(0xFFFFFFFFu, until, 31);
+  const u64 target = min(__umul64hi(chance, total), total - 1);
+  int at = -1;
+  u64 before = until - f.sum();
 #pragma unroll
-          for (int j = 0; j < kHold; ++j) {
-            float x[kN];
-            Vec<T>::unpack(v[j], x);
+  for (int i = 0; i < 4; ++i) {
+    if (at < 0 && target >= before && target - before < f.v[i]) at = 4 * lane + i;
+    if (at < 0) before += f.v[i];
+  }
+  const int l0 = __ffs(__ballot_sync(0xFFFFFFFFu, at >= 0)) - 1;
+  at = __shfl_sync(0xFFFFFFFFu, at, l0);
+  before = __shfl_sync(0xFFFFFFFFu, before, l0);
+  if (at / kWarps != (int)cl.rank) return total;
+  const int end = min(sl.groups, (at % kWarps + 1) * sl.run());
+  for (int g0 = at % kWarps * sl.run(); g0 < end; g0 += kThreads * kHold) {
+    // a thread takes up to kHold neighbouring groups
+    const int hold = min(kHold, (end - g0 + kThreads - 1) / kThreads), first = g0 + (int)threadIdx.x * hold;
+    uint4 v[kHold];
+    u64 sum = 0;
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (x[i] >= theta) {
-                c += weight(x[i]);
-                if (token < 0 && c > target) token = (int)(lo + (first + j) * kN - sl.head + i);
-              }
-          }
-          a.tokens[t] = token;
-          if (probs && greedy)
-            for (uint32_t r = 0; r < cl.size; ++r) cluster_st(cluster_map(&s.token, r), (uint32_t)token);
-        }
-        before += all;
-        if (before > target) break;
+    for (int j = 0; j < kHold; ++j) v[j] = j < hold && first + j < end ? sl.template raw<kResident>(first + j) : sl.nothing();
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+      float x[kN];
+      R::V::unpack(v[j], x);
+      if (max_of(x) >= theta) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) sum += x[i] >= theta ? row.weight(x[i]) : 0;
       }
     }
+    u64 upto = scan_add(sum);
+    __syncthreads();
+    if (lane == 31) row.s->scan[warp] = upto;
+    __syncthreads();
+    u64 all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const u64 o = row.s->scan[w];
+      if (w < warp) upto += o;
+      all += o;
+    }
+    upto += before;
+    if (target >= upto - sum && target < upto) {
+      u64 c = upto - sum;
+      int token = -1;
+#pragma unroll
+      for (int j = 0; j < kHold; ++j) {
+        float x[kN];
+        R::V::unpack(v[j], x);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (x[i] >= theta) {
+            c += row.weight(x[i]);
+            if (token < 0 && c > target) token = row.lo + (first + j) * kN - sl.head + i;
+          }
+      }
+      a.tokens[t] = token;
+      if (tell_all)
+        for (uint32_t r = 0; r < cl.size; ++r) cluster_st(cluster_map(&row.s->token, r), (uint32_t)token);
+    }
+    before += all;
+    if (before > target) break;
+  }
+  return total;
+}
+
+// ---------------------------------------------------------------------------
+// The kernel.  kFilters: some row may have a top-k or top-p; without, it is
+// leaner (no lists, fewer registers), which the rows that only stream feel.
+// ---------------------------------------------------------------------------
+struct Nothing {};
+
+template <typename T, bool kResident, bool kFilters>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+  extern __shared__ __align__(16) uint4 s_stage[];
+  __shared__ Shared s;
+  __shared__ typename std::conditional<kFilters, Lists, Nothing>::type f;
+  constexpr int kN = Vec<T>::kN;
+  Row<T, kResident> row;
+  Cluster& cl = row.cl;
+  cl = Cluster{&s, cluster_rank(), cluster_size(), 0};
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the first meeting
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = (int)(blockIdx.x / cl.size);
+  row.s = &s;
+  row.lo = (int)cl.rank * a.slice;
+  Slice<T>& sl = row.sl;
+  sl.src = static_cast<const T*>(a.logits) + t * a.row_stride + row.lo;
+  sl.stage = s_stage;
+  sl.n = max(0, min(a.slice, a.V - row.lo));
+  sl.head = (int)((reinterpret_cast<uintptr_t>(sl.src) & 15u) / sizeof(T));
+  sl.groups = sl.n > 0 ? (sl.head + sl.n + kN - 1) / kN : 0;
+
+  // the row's settings
+  const float u = __ldg(a.uniforms + t);
+  float tau = a.temperature ? __ldg(a.temperature + t) : a.temperature_all;
+  float min_p = a.min_p ? __ldg(a.min_p + t) : a.min_p_all;
+  float top_p = 1.f;
+  int top_k = 0;
+  if constexpr (kFilters) {
+    top_p = a.top_p ? __ldg(a.top_p + t) : a.top_p_all;
+    top_k = a.top_k ? __ldg(a.top_k + t) : a.top_k_all;
+  }
+  s.table[threadIdx.x] = kExp2.v[threadIdx.x];
+  if constexpr (kResident) {
+    if (!row.stage() && a.status) atomicOr(a.status, SV_DEV_TIMEOUT);
+  }
+  row.find_top();
+  // rows that are not on the GPU yet start on their way into L2
+  if (!kResident && a.ahead > 0 && t + a.ahead < a.rows) prefetch_row<T>(sl, a.ahead * a.row_stride);
+
+  const bool greedy = tau < kColdest;
+  if (greedy) {
+    tau = 1.f;
+    top_k = 0;
+    top_p = 1.f;
+    min_p = 1.f;
+  }
+  if (top_k >= a.V) top_k = 0;
+  if (min_p > 0.f && threadIdx.x == 0) {
+    // the distance from m at which min-p cuts, as a pair
+    const double ln = min_p >= 1.f ? 0.0 : (a.min_p ? log((double)min_p) : a.ln_min_p_all);
+    const double d = (double)tau * fmax(ln, -kSupportBits * 0.69314718055994530942);
+    s.delta[0] = (float)d;
+    s.delta[1] = (float)(d - (double)(float)d);
+  }
+  if constexpr (kFilters)
+    if (threadIdx.x == 0) f.count = 0;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the cluster runs
+
+  // the row's largest logit and, with a small top-k, a bound that top_k logits reach
+  float bound = -INFINITY;
+  const int rounds = publish_rounds(top_k, cl.slots());
+  if constexpr (kFilters) {
+    if (rounds > 0) bound = publish(row, f, rounds, top_k);
+  }
+  if (rounds == 0) row.m = key_float(cl.max(key_of(row.top_here)));
+  float* const probs = a.probs ? a.probs + (long long)t * a.V + row.lo : nullptr;
+  if (!(fabsf(row.m) < INFINITY) || !(tau <= kHottest)) {
+    // nothing to draw from: no finite largest logit, or no temperature
+    if (probs)
+      for (int i = threadIdx.x; i < sl.n; i += kThreads) probs[i] = 0.f;
+    if (cl.rank == 0 && threadIdx.x == 0) {
+      a.tokens[t] = -1;
+      if (a.status) atomicOr(a.status, SV_DEV_BAD_LOGITS);
+    }
+    return;
+  }
+  row.set_weight(tau, a.down);
+  float theta = row.rw.least;  // what the support and the filters so far keep
+  if (min_p > 0.f) theta = fmaxf(theta, add_up(row.m, s.delta[0], s.delta[1]));
+  const u64 chance = greedy ? 0 : fraction64(u);
+  u64 total = 0, mine = 0;
+  bool drawn = false, summed = false;
+  if constexpr (kFilters) {
+    if (bound > -INFINITY) drawn = small_top_k(row, f, a, t, top_k, bound, top_p, chance, &theta, &total);
+    if (!drawn) {
+      float base = row.rw.least;
+      if (top_k > 0) {
+        base = fmaxf(base, find_border<false>(row, f, base, top_k, 0.f).x);
+        theta = fmaxf(theta, base);
+      }
+      if (top_p < 1.f) {
+        const Border b = find_border<true>(row, f, base, 0, top_p);
+        // where min-p cuts no further, the weight above the window and the
+        // warp's own among this CTA's candidates make up what it keeps
+        summed = b.ready && b.x >= theta;
+        theta = fmaxf(theta, b.x);
+        if (summed) {
+          mine = b.here;
+          const int from = warp * sl.run() * kN - sl.head, to = sl.run_end() * kN - sl.head;
+          for (int i = lane; i < f.count; i += 32) {
+            const float x = key_float((uint32_t)(f.cand[i] >> 32));
+            const int at = (int)(uint32_t)f.cand[i] - row.lo;
+            if (x >= theta && at >= from && at < to) mine += row.weight(x);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  if (!drawn) {
+    if (!summed)
+      row.reaching(theta, [&](const float(&x)[kN], int) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const u64 w = row.weight(x[i]);
+          mine += x[i] >= theta ? w : 0;
+        }
+      });
+    total = draw(row, a, t, theta, mine, chance, greedy && probs);
   }
   if (!probs) return;
   if (greedy) {
     cl.sync();  // the token is known
-    for (int i = threadIdx.x; i < sl.n; i += kThreads) probs[i] = lo + i == s.token ? 1.f : 0.f;
+    for (int i = threadIdx.x; i < sl.n; i += kThreads) probs[i] = row.lo + i == s.token ? 1.f : 0.f;
     return;
   }
-  if (threadIdx.x == 0) s.delta[0] = (float)(1.0 / (double)total);
+  if (threadIdx.x == 0) s.inv_total = (float)(1.0 / (double)total);
   __syncthreads();
-  const float inv = s.delta[0];
+  const float inv = s.inv_total;
   const bool wide = ((reinterpret_cast<uintptr_t>(probs) - 4u * sl.head) & 15u) == 0;  // groups at 16-byte addresses
   const int run_end = sl.run_end();
   sl.template own<kResident, 2>([&](const float(&x)[kN], int i0, int g) {
-    if (g >= run_end) return;
+    if (g >= run_end) return;  // another's
     float p[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) p[i] = 0.f;
@@ -1167,7 +1277,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
       for (int i = 0; i < kN; ++i)
         if (x[i] >= theta) {
-          const Weight w = weight_of(rw, s.table, x[i]);
+          const Weight w = weight_of(row.rw, s.table, x[i]);
           p[i] = (float)w.mant * __uint_as_float((uint32_t)(127 + 31 - w.shift) << 23) * inv;
         }
     }
@@ -1185,7 +1295,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 
 // ------------------------------------------------------------------ host side
 // two CTAs share an SM's 228 KB, of which each CTA takes 1 KB more than it asks for
-constexpr size_t kStage = (114 * 1024 - 1024 - sizeof(Shared) - 64) / 16 * 16;
+constexpr size_t kStage = (114 * 1024 - 1024 - sizeof(Shared) - sizeof(Lists) - 128) / 16 * 16;
 
 struct Shape {
   int ctas, slice;
@@ -1208,9 +1318,9 @@ Shape row_shape(int T, int V, int elem) {
   return sh;
 }
 
-template <typename T, bool kResident>
+template <typename T, bool kResident, bool kFilters>
 cudaError_t launch_sample(const SampleArgs& a, int rows, const Shape& sh, cudaStream_t st) {
-  auto kernel = sample_kernel<T, kResident>;
+  auto kernel = sample_kernel<T, kResident, kFilters>;
   if (kResident) {
     static std::atomic<bool> done[64];  // per instance and device
     int dev = 0;
@@ -1235,6 +1345,13 @@ cudaError_t launch_sample(const SampleArgs& a, int rows, const Shape& sh, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T>
+cudaError_t launch_for(const SampleArgs& a, int rows, const Shape& sh, bool filters, cudaStream_t st) {
+  if (filters)
+    return sh.stage ? launch_sample<T, true, true>(a, rows, sh, st) : launch_sample<T, false, true>(a, rows, sh, st);
+  return sh.stage ? launch_sample<T, true, false>(a, rows, sh, st) : launch_sample<T, false, false>(a, rows, sh, st);
 }
 
 inline bool off_by(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
@@ -1284,11 +1401,8 @@ extern "C" sv_status sample_tokens(const void* logits, int logits_type, int T, i
   a.down = 0;
   while ((1 << a.down) < V) ++a.down;  // V <= 2^down: V (2^63 >> down) <= 2^63
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (elem == 4)
-    e = sh.stage ? launch_sample<float, true>(a, T, sh, st) : launch_sample<float, false>(a, T, sh, st);
-  else
-    e = sh.stage ? launch_sample<__nv_bfloat16, true>(a, T, sh, st) : launch_sample<__nv_bfloat16, false>(a, T, sh, st);
+  const bool filters = top_k || top_k_all > 0 || top_p || top_p_all < 1.f;
+  const cudaError_t e = elem == 4 ? launch_for<float>(a, T, sh, filters, st) : launch_for<__nv_bfloat16>(a, T, sh, filters, st);
   if (e == cudaSuccess) return SV_OK;
   cudaGetLastError();
   return SV_ERR_LAUNCH;
