@@ -785,8 +785,9 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
   });
   cl.sync();
   // CTA r adds up share r of the bins (from the largest weights down), thread i
-  // of it `per` bins, so that the slots of a meeting are in bin order too.  A
-  // share's sums stay in its CTA's own histogram, where no other CTA reads now.
+  // of it `per` bins, so that the slots of a meeting are in bin order too.  The
+  // sums go back to where the parts came from (nobody else reads them there), so
+  // that every CTA has the row's histogram.
   const int own = kBins / (int)cl.size;
   const int per = (own + kThreads - 1) / kThreads;
   constexpr int kPer = (kBins + kThreads - 1) / kThreads;
@@ -804,7 +805,9 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
         c[0] = f.hist[bin];
 #pragma unroll
         for (uint32_t r = 1; r < kClusterMax; ++r) c[0] += c[r];
-        f.hist[bin] = c[0];
+#pragma unroll
+        for (uint32_t r = 0; r < kClusterMax; ++r)
+          if (r < cl.size) cluster_st(cluster_map(f.hist + bin, cl.rank ^ r), c[0]);
         n += c[0] & kCountMask;
         e += bin_estimate(c[0], bin);
       }
@@ -871,7 +874,7 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
     float est[kPer], e_here = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      word[i] = i < per && first + i < own ? cluster_ld(f.hist + bin0 + i, (uint32_t)owner) : 0;
+      word[i] = i < per && first + i < own ? f.hist[bin0 + i] : 0;
       est[i] = bin_estimate(word[i], bin0 + i);
       n_here += word[i] & kCountMask;
       e_here += est[i];
