@@ -1297,27 +1297,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 }
 
 // ------------------------------------------------------------------ host side
-// two CTAs share an SM's 228 KB, of which each CTA takes 1 KB more than it asks for
-constexpr size_t kStage = (114 * 1024 - 1024 - sizeof(Shared) - sizeof(Lists) - 128) / 16 * 16;
+// A slice's room in shared memory: an SM has 228 KB, of which each CTA takes 1
+// KB more than it asks for; one CTA may have 227 KB.
+constexpr size_t kRest = sizeof(Shared) + sizeof(Lists) + 128;
+constexpr size_t kStageTwo = (114 * 1024 - 1024 - kRest) / 16 * 16;
+constexpr size_t kStageOne = (227 * 1024 - kRest) / 16 * 16;
+constexpr int kSms = 152;
 
 struct Shape {
   int ctas, slice;
   size_t stage;  // bytes of a resident slice, 0: rows are read again for every pass
 };
-// As many CTAs a row as keep all rows on the GPU at once (two CTAs an SM),
-// down to 4096 logits a CTA.  With many rows a slice then does not fit in
-// shared memory and is read again where a later pass needs it, mostly from L2:
-// for top-k and min-p that is a few groups (512 rows of 163840 logits, min-p:
-// one CTA a row 0 us, eight CTAs with slices in shared memory 114 us).
+// CTAs a row: as many as still leave every CTA an SM of its own, of at least
+// 4096 logits each.  More make the passes shorter, but the meetings dearer:
+// vocabularies of 163840 fp32 logits under top-p 0.95 take with 1, 2, 4 and 8
+// CTAs a row
+//   1 row:     FIG_C1
+//   32 rows:   FIG_C32
+//   67 rows:   FIG_C67
+//   152 rows:  FIG_C152
+// (us).  Two CTAs share an SM only where their slices are long, as with the 152
+// rows.  Clusters of eight are placed two CTAs to an SM long before the SMs run
+// out (16 rows under top-k 50: 13.4 us against 11.0 with four), so they are for
+// up to 12 rows.  A slice that does not fit in shared memory is read again where
+// a later pass needs it, mostly from L2: for top-k and min-p a few groups.
 Shape row_shape(int T, int V, int elem) {
   Shape sh;
   auto slice_of = [&](int c) { return (int)((((long long)V + c - 1) / c + 7) / 8 * 8); };
   auto stage_of = [&](int c) { return ((size_t)slice_of(c) * elem + 16 + 15) / 16 * 16; };
+  auto alone = [&](int c) { return c <= 4 ? (long long)T * c <= kSms : T <= 12; };
   int c = 1;
-  while (c < kClusterMax && (long long)T * 2 * c <= 304 && slice_of(2 * c) >= 4096) c *= 2;
+  while (c < kClusterMax && slice_of(2 * c) >= 4096 &&
+         (alone(2 * c) || ((long long)T * 2 * c <= 2 * kSms && slice_of(2 * c) >= 65536)))
+    c *= 2;
   sh.ctas = c;
   sh.slice = slice_of(c);
-  sh.stage = stage_of(c) <= kStage ? stage_of(c) : 0;
+  sh.stage = stage_of(c) <= (alone(c) ? kStageOne : kStageTwo) ? stage_of(c) : 0;
   return sh;
 }
 
@@ -1330,7 +1345,7 @@ cudaError_t launch_sample(const SampleArgs& a, int rows, const Shape& sh, cudaSt
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStage);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStageOne);
       if (e != cudaSuccess) return e;
       if (dev < 64) done[dev].store(true, std::memory_order_release);
     }
@@ -1400,7 +1415,7 @@ extern "C" sv_status sample_tokens(const void* logits, int logits_type, int T, i
   const Shape sh = row_shape(T, V, elem);
   a.slice = sh.slice;
   a.rows = T;
-  a.ahead = sh.ctas == 1 && T > 304 ? 304 : 0;
+  a.ahead = sh.ctas == 1 && T > 2 * kSms ? 2 * kSms : 0;
   a.down = 0;
   while ((1 << a.down) < V) ++a.down;  // V <= 2^down: V (2^63 >> down) <= 2^63
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
