@@ -38,9 +38,9 @@
 //    is inside, whose weights every CTA then adds up.
 //  * Where the window holds too many (ties): quartering of the logits' bits.
 // What bounds it: with many rows HBM (512 rows of 163840 fp32 logits under a
-// min-p: FIG_BATCH us, FIG_BATCHBW TB/s), or under top-p instruction issue (about 45
+// min-p: 64 us, 5.2 TB/s), or under top-p instruction issue (about 45
 // instructions a logit, 32 of them its weight); with few rows the latency of
-// the meetings (one row under top-k 50, top-p 0.9: FIG_ONE us).
+// the meetings (one row under top-k 50, top-p 0.9: 9.5 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1308,28 +1308,30 @@ struct Shape {
   int ctas, slice;
   size_t stage;  // bytes of a resident slice, 0: rows are read again for every pass
 };
-// CTAs a row: as many as still leave every CTA an SM of its own, of at least
-// 4096 logits each.  More make the passes shorter, but the meetings dearer:
-// vocabularies of 163840 fp32 logits under top-p 0.95 take with 1, 2, 4 and 8
-// CTAs a row
-//   1 row:     FIG_C1
-//   32 rows:   FIG_C32
-//   67 rows:   FIG_C67
-//   152 rows:  FIG_C152
-// (us).  Two CTAs share an SM only where their slices are long, as with the 152
-// rows.  Clusters of eight are placed two CTAs to an SM long before the SMs run
-// out (16 rows under top-k 50: 13.4 us against 11.0 with four), so they are for
-// up to 12 rows.  A slice that does not fit in shared memory is read again where
-// a later pass needs it, mostly from L2: for top-k and min-p a few groups.
-Shape row_shape(int T, int V, int elem) {
+// CTAs a row.  More make a row's passes shorter, but its meetings dearer, and
+// two CTAs on an SM get in each other's way.  So: as many as leave every CTA an
+// SM of its own, of at least 4096 logits each; where every logit's weight is
+// needed (`heavy`: top-p over the vocabulary, or no filter) up to two CTAs an SM,
+// of at least 16384 logits.  In us with 1, 2, 4 and 8 CTAs a row of 163840 fp32
+// logits:
+//   min-p, 1 row 14 10 8 7, 32 rows 15 10 8 9, 67 rows 15 10 11 17, 152 rows 19 18 27 36
+//   top-p 0.95 with probs, 32 rows 145 83 44 40, 64 rows 149 84 61 69
+// and 67 mixed rows of 32003 bf16 33 21 26 37.  (Clusters of eight are placed two
+// CTAs to an SM long before the SMs run out: 16 rows under top-k 50 take 13.4 us
+// with eight CTAs a row, 11.0 with four.)  A slice that does not fit in shared
+// memory is read again where a later pass needs it, mostly from L2: for top-k
+// and min-p a few groups.
+Shape row_shape(int T, int V, int elem, bool heavy) {
   Shape sh;
   auto slice_of = [&](int c) { return (int)((((long long)V + c - 1) / c + 7) / 8 * 8); };
   auto stage_of = [&](int c) { return ((size_t)slice_of(c) * elem + 16 + 15) / 16 * 16; };
   auto alone = [&](int c) { return c <= 4 ? (long long)T * c <= kSms : T <= 12; };
+  auto worth = [&](int c) {
+    return (alone(c) && slice_of(c) >= 4096) ||
+           ((long long)T * c <= 2 * kSms && slice_of(c) >= (heavy ? 16384 : 65536));
+  };
   int c = 1;
-  while (c < kClusterMax && slice_of(2 * c) >= 4096 &&
-         (alone(2 * c) || ((long long)T * 2 * c <= 2 * kSms && slice_of(2 * c) >= 65536)))
-    c *= 2;
+  while (c < kClusterMax && worth(2 * c)) c *= 2;
   sh.ctas = c;
   sh.slice = slice_of(c);
   sh.stage = stage_of(c) <= (alone(c) ? kStageOne : kStageTwo) ? stage_of(c) : 0;
@@ -1412,14 +1414,16 @@ extern "C" sv_status sample_tokens(const void* logits, int logits_type, int T, i
   a.tokens = tokens;
   a.probs = probs;
   a.status = status;
-  const Shape sh = row_shape(T, V, elem);
+  const bool filters = top_k || top_k_all > 0 || top_p || top_p_all < 1.f;
+  const bool small_k = !top_k && top_k_all > 0 && top_k_all <= kPublished / 2;
+  const bool floored = min_p || min_p_all > 0.f || (!temperature && temperature_all < kColdest);
+  const Shape sh = row_shape(T, V, elem, filters ? (top_p || top_p_all < 1.f) && !small_k : !floored);
   a.slice = sh.slice;
   a.rows = T;
   a.ahead = sh.ctas == 1 && T > 2 * kSms ? 2 * kSms : 0;
   a.down = 0;
   while ((1 << a.down) < V) ++a.down;  // V <= 2^down: V (2^63 >> down) <= 2^63
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool filters = top_k || top_k_all > 0 || top_p || top_p_all < 1.f;
   const cudaError_t e = elem == 4 ? launch_for<float>(a, T, sh, filters, st) : launch_for<__nv_bfloat16>(a, T, sh, filters, st);
   if (e == cudaSuccess) return SV_OK;
   cudaGetLastError();
