@@ -230,6 +230,84 @@ def test_repeat_streams_and_graph(sv):
         assert torch.equal(tokens, want[i][0]) and torch.equal(probs, want[i][1])
 
 
+@pytest.mark.parametrize("T,V", [(1, 32773), (12, 65521), (13, 65521), (38, 40001), (76, 70001), (76, 20001), (152, 12289), (153, 9000), (320, 4096)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_work_split(sv, T, V, dtype):
+    """Rows split into eight, four, two and one parts, resident or not, on both
+    sides of where the split changes: the only logit of weight lies at the
+    first and the last place of every part of 1/8 (and so of every other), at
+    the row's ends, and the rows also carry a common distribution."""
+    rng = np.random.default_rng(T + V)
+    x = np.full((T, V), -80.0, np.float32)
+    ends = sorted({min(max(c, 0), V - 1) for n in (1, 2, 4, 8) for i in range(n + 1) for c in
+                   (lambda q: (q - 1, q))(i * ((((V + n - 1) // n) + 7) // 8 * 8))})
+    at = np.array([ends[t % len(ends)] for t in range(T)])
+    x[np.arange(T), at] = 3.0
+    u = rng.random(T).astype(np.float32)
+    for s in (dict(), dict(top_k=3), dict(top_p=0.99), dict(top_k=600, top_p=0.9), dict(min_p=0.5)):
+        assert np.array_equal(run(sv, dev(x).to(dtype), u, s, probs=False), at)
+    check(sv, dev(logits(rng, T, V)).to(dtype), u, settings(rng, "mixed", T))
+
+
+@pytest.mark.parametrize("T", [1, 40, 160])
+@pytest.mark.parametrize("kind", ["band", "few", "ends", "falling"])
+def test_crowded_borders(sv, kind, T):
+    """Where the estimate of a border from the counts goes wrong or the window
+    around it holds more than can be listed: a band of distinct logits narrower
+    than a step of the weight's grid (2^(1/512)); a band of some hundred; logits
+    at both ends of one histogram bin, none between, so that its middle is a bad
+    guess; a distribution in which every bin falls steeply."""
+    rng = np.random.default_rng(len(kind) + T)
+    V = 30011
+    x = rng.standard_normal((T, V)) - 6
+    if kind == "band":
+        x[:, 100:28000] = 1 + 1e-3 * rng.random((T, 27900))
+    elif kind == "few":
+        x[:, rng.permutation(V)[:1700]] = 1 + 1e-3 * rng.random((T, 1700))
+    elif kind == "ends":
+        step = np.log(2) / 512
+        x[:, ::2] = np.where(rng.random((T, V - V // 2)) < 0.5, 0.3, 7.6) * step + 1e-5 * rng.random((T, V - V // 2))
+        x[:, 7] = 40 * step
+    else:
+        x = -np.abs(rng.standard_normal((T, V))) ** 0.25 * 4
+    x = dev(x.astype(np.float32))
+    u = rng.random(T).astype(np.float32)
+    for s in (dict(top_p=0.3), dict(top_p=0.77), dict(top_k=1200, top_p=0.6), dict(top_k=9000), dict(top_k=40), dict(top_k=16000, temperature=0.5)):
+        check(sv, x, u, s)
+
+
+def test_more_equal_than_candidates(sv):
+    """A top-k whose last place is shared by more logits than can be ranked in
+    one CTA: they are all kept."""
+    rng = np.random.default_rng(21)
+    for T, V in ((2, 40000), (60, 40000), (160, 3001)):
+        x = logits(rng, T, V, spread=0.1, peaks=5)
+        x[:, 10:1210] = 2.0
+        s = dict(top_k=50)
+        check(sv, dev(x), rng.random(T).astype(np.float32), s)
+        assert np.all((run(sv, dev(x), rng.random(T).astype(np.float32), s)[1] > 0).sum(1) >= 1200)
+
+
+def test_repeated_calls_agree(sv):
+    """Nothing of a call is left for the next: calls of different shapes and
+    settings in turn, on two streams at once, give each time the same bits."""
+    rng = np.random.default_rng(22)
+    calls = []
+    for T, V, mode in ((3, 40000, "kpm"), (200, 9000, "p"), (40, 163840, "mixed"), (400, 4099, "plain")):
+        calls.append((dev(logits(rng, T, V)), dev(rng.random(T).astype(np.float32)), {k: dev(v) for k, v in settings(rng, mode, T).items()}))
+    want = [sv.sample_tokens(x, u, return_probs=True, **s) for x, u, s in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for turn in range(3):
+        got = []
+        for i, (x, u, s) in enumerate(calls * 2):
+            with torch.cuda.stream(streams[(i + turn) % 2]):
+                got.append(sv.sample_tokens(x, u, return_probs=True, **s))
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert torch.equal(g[0], want[i % 4][0]) and torch.equal(g[1], want[i % 4][1])
+
+
 def test_refusals(sv):
     x, u = torch.zeros((4, 100), device=DEV), torch.zeros(4, device=DEV)
     k = torch.ones(4, dtype=torch.int32, device=DEV)
@@ -252,6 +330,7 @@ def test_drafts_drawn_then_verified(sv):
     has every draft accepted (u q(d) < p(d) for u < 1), one that never agrees
     has none."""
     rng = np.random.default_rng(14)
+    torch.manual_seed(14)
     R, k, V, P, mp = 6, 3, 5000, 40, 4
     refs, table, lens = (torch.zeros(P, dtype=torch.int32, device=DEV), torch.full((R, mp), -1, dtype=torch.int32, device=DEV),
                          torch.zeros(R, dtype=torch.int32, device=DEV))
