@@ -332,7 +332,7 @@ sv_status mla_kv_append(const void* kv_new, const int32_t* positions, const int3
  * state after the call is written to the *_out arrays, whole; an *_out pointer
  * may be the *_in pointer (update in place), other overlaps are not allowed.
  * page_size must be 64.  R * max_pages_per_req and max_pages_per_req * 64
- * must be below 2^31.
+ * must be below 2^31, R and the forks of a call at most 2^30.
  *
  *   workspace  at least sv_kv_pages_workspace_bytes(num_pages, R, n) bytes
  *              (n: forks of a kv_pages_fork call, 0 otherwise), 256-byte
@@ -359,12 +359,13 @@ sv_status mla_kv_append(const void* kv_new, const int32_t* positions, const int3
  *   the parent's length and full pages, whose counts grow by one, and a page of
  *   its own with a copy of the rows in use of the parent's last, partly filled
  *   page (the other rows of that page keep what they hold).  So neither
- *   writes into a page of the other when both go on.  A child must hold nothing (length 0); when a child is named
- *   twice only the first fork counts.  A fork with an index outside [0, R), a
- *   child in use or named before (SV_DEV_BAD_REQUEST), a parent's length out
- *   of range or no page left for its last rows (SV_DEV_NO_PAGE) leaves the
- *   child as it was.  A parent's entry outside the pool is passed on as it is
- *   (SV_DEV_BAD_PAGE), counted nowhere and copied from nowhere.
+ *   writes into a page of the other when both go on.  A child must hold nothing
+ *   (length 0); when a child is named twice only the first fork counts.  A fork
+ *   with an index outside [0, R), a child in use or named before
+ *   (SV_DEV_BAD_REQUEST), a parent's length out of range or no page left for
+ *   its last rows (SV_DEV_NO_PAGE) leaves the child as it was.  A parent's entry
+ *   outside the pool is passed on as it is (SV_DEV_BAD_PAGE), counted nowhere
+ *   and copied from nowhere.
  *   Two kernels on `stream` (the second a programmatic dependent launch).
  *
  * kv_pages_resize: request r gets the pages of length new_lens[r] (-1: stays
@@ -549,7 +550,7 @@ sv_status spec_verify_sampled(const float* logits, int R, int k, int V, float te
  *                fp32), or NULL to take the *_all value for every row.
  *   tokens       int32 [T];  probs fp32 [T][V], may be NULL.
  *   status       device int32, may be NULL.
- * No workspace; one kernel on `stream`.
+ * No output may overlap an input.  No workspace; one kernel on `stream`.
  * ---------------------------------------------------------------------- */
 sv_status sample_tokens(const void* logits, int logits_type, int T, int V, long long row_stride,
                         const float* uniforms, const float* temperature, float temperature_all,

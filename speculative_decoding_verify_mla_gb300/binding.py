@@ -610,6 +610,8 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature=1.0,
         row = V
     elif row < V:
         raise ValueError("rows of logits must not overlap")
+    if not isinstance(top_k, torch.Tensor):
+        top_k = max(0, min(top_k, V))  # an int of any size
     if tokens is None:
         tokens = torch.empty(T, dtype=_INT32, device=logits.device)
     if probs is None:

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kMetaThreads) resize_kernel(const ResizeArgs a
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const Change c = change_of(a, old_len[i], new_len[i], row[i] >= 0 && at[i] == 0);
+      const Change c = change_of(a, old_len[i], new_len[i], false);
       want[i] = c.want;
       have[i] = c.have;
     }
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kMetaThreads) resize_kernel(const ResizeArgs a
   group_sync(g);
   // hand out: a warp per request
   for (int r = tid >> 5; r < a.R; r += threads >> 5) {
-    const Change c = read_change(a, r, false);
+    const Change c = read_change(a, r, lane == 0);
     bool done = may_grow(a, r, c, lane == 0);
     if (done && c.want > c.have) {
       const int first = __ldcg(a.prefix + r);
@@ -717,6 +717,7 @@ cudaError_t launch_meta(void (*kernel)(Args), const Args& a, long long words, cu
 // us).  Where the number of moves is only known on the device the grid is for
 // at most kMoveCtas of them, the rest by looping.
 constexpr long long kMostCtas = 0x7FFFFFFF;
+constexpr int kMostRows = 1 << 30;  // requests or forks of a call: their loops' counters stay int
 constexpr long long kMoveCtas = 152 * 8 * 24;
 
 template <class... Ts, class... Us>
@@ -737,7 +738,7 @@ inline unsigned copy_ctas(long long items, long long most) { return (unsigned)(i
 
 // The checks that the bookkeeping calls share.
 sv_status check_tables(int num_pages, int page_size, int R, int mp, const void* const* needed, int count) {
-  if (num_pages < 1 || R < 0 || mp < 0) return SV_ERR_SHAPE;
+  if (num_pages < 1 || R < 0 || R > kMostRows || mp < 0) return SV_ERR_SHAPE;
   if (page_size != SV_PAGE_SIZE) return SV_ERR_UNSUPPORTED;
   if ((long long)R * mp > 0x7FFFFFFFll || (long long)mp * SV_PAGE_SIZE > 0x7FFFFFFFll) return SV_ERR_SHAPE;
   for (int i = 0; i < count; ++i)
@@ -830,7 +831,7 @@ extern "C" sv_status kv_pages_fork(void* kv_pages, int num_pages, int page_size,
   using namespace sv;
   const void* needed[] = {ref_counts_in, ref_counts_out, block_table_in, block_table_out,
                           kv_lens_in,    kv_lens_out,    parents,        children};
-  if (n < 0 || (n > 0 && (R < 1 || max_pages_per_req < 1))) return SV_ERR_SHAPE;
+  if (n < 0 || n > kMostRows || (n > 0 && (R < 1 || max_pages_per_req < 1))) return SV_ERR_SHAPE;
   const bool rows = R > 0 && max_pages_per_req > 0;
   sv_status e = check_tables(num_pages, page_size, R, max_pages_per_req, needed, rows ? (n > 0 ? 8 : 6) : 2);
   if (e != SV_OK) return e;

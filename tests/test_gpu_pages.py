@@ -231,6 +231,15 @@ def test_empty_calls(sv):
         check(got[0:1] + got[2:], ([1, 2, 0, 0], [0, -1, 1, -1], [2]))
 
 
+def test_tables_without_entries(sv):
+    """Requests that can hold nothing: a length other than 0 is out of range."""
+    refs, table, lens = i32(np.zeros(5)), i32(np.zeros((3, 0))), i32(np.zeros(3))
+    for new, bit in (([0, -1, 0], 0), ([0, 1, 0], sv.SV_DEV_BAD_BOUND), ([-2, 0, 0], sv.SV_DEV_BAD_BOUND)):
+        status = i32([0])
+        got = sv.kv_pages_resize(refs, table, lens, i32(new), status=status)
+        assert got[2].tolist() == [0, 0, 0] and got[0].tolist() == [0] * 5 and status.item() == bit
+
+
 def test_refusals(sv):
     refs, table, lens = i32(np.zeros(8)), i32(np.zeros((2, 3))), i32([0, 0])
     pool = torch.zeros((8, 64, 512), dtype=torch.bfloat16, device=DEV)

@@ -308,6 +308,13 @@ def test_repeated_calls_agree(sv):
             assert torch.equal(g[0], want[i % 4][0]) and torch.equal(g[1], want[i % 4][1])
 
 
+def test_top_k_past_32_bits(sv):
+    x, u = dev(logits(np.random.default_rng(23), 3, 900)), torch.rand(3, device=DEV)
+    for k, same in ((2 ** 32 + 5, 0), (2 ** 31, 0), (-2 ** 32 + 5, 0), (899, 899)):
+        got, want = (sv.sample_tokens(x, u, top_k=v, return_probs=True) for v in (k, same))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_refusals(sv):
     x, u = torch.zeros((4, 100), device=DEV), torch.zeros(4, device=DEV)
     k = torch.ones(4, dtype=torch.int32, device=DEV)

@@ -63,6 +63,14 @@ def test_resize_checks(lib):
     assert call(_6=0, _4=None) == 1  # no entries, but lengths
 
 
+def test_most_requests(lib):
+    assert lib.kv_pages_resize(*[A, 64, 64, A, A, (1 << 30) + 1, 1, A, A, A, A, A, 1 << 40, None, None]) == 2
+    fork = [A, 64, 64, 2, 1024, A, A, A, 4, 8, A, A, (1 << 30) + 1, A, A, A, A, 1 << 40, None, None]
+    assert lib.kv_pages_fork(*fork) == 2
+    fork[8:10], fork[12] = [(1 << 30) + 1, 1], 2
+    assert lib.kv_pages_fork(*fork) == 2
+
+
 def test_fork_and_compact_checks(lib):
     ok = [A, 64, 64, 2, 1024, A, A, A, 4, 8, A, A, 2, A, A, A, A, 1 << 20, None, None]
 
