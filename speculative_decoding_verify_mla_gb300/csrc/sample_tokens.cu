@@ -76,10 +76,13 @@ constexpr int kBins = 2592;      // bins of 1/64 octave of weight: 40.5 octaves,
 constexpr int kMargin = 64;      // logits on both sides of the place where top-p's border is expected
 constexpr int kTries = 2;        // guesses of it before the quartering
 
-// round(2^31 2^(j/512)), j = 0..511, by the exponential series.
+// round(2^31 2^(j/512)), j = 0..511, by the exponential series: {the integer
+// less kMagicBits, its fp32 as bits}.
 constexpr int kGrid = 512, kGridBits = 9;
+constexpr uint32_t kMagicBits = 0x4B400000u;  // of 12582912.f = 1.5 * 2^23
+constexpr uint32_t kGridZero = 0x46C00000u;   // of 24576.f = 1.5 * 2^14: the place of t = 0
 struct Exp2Table {
-  uint32_t v[kGrid];
+  uint2 v[kGrid];
   constexpr Exp2Table() : v() {
     for (int j = 0; j < kGrid; ++j) {
       const double y = j * 0.693147180559945309417232121458 / kGrid;
@@ -88,7 +91,9 @@ struct Exp2Table {
         term *= y / i;
         sum += term;
       }
-      v[j] = (uint32_t)(sum * 2147483648.0 + 0.5);
+      const uint32_t t = (uint32_t)(sum * 2147483648.0 + 0.5);
+      v[j].x = t - kMagicBits;
+      v[j].y = ((t + 128) >> 8) + 0x4E800000u;  // 2^31 <= t, t + 128 < 2^32
     }
   }
 };
@@ -148,12 +153,11 @@ struct SampleArgs {
 
 // Shared memory of every row, and of rows with top-k or top-p.
 struct Shared {
-  uint32_t table[kGrid];
+  uint2 table[kGrid];
   __align__(16) u64 slot[2][3][kSlots];  // meetings: parity, value, (rank, warp)
   u64 scan[kWarps];
   u64 bar[kPieces];                      // arrival of the slice's pieces
   float delta[2];
-  float inv_total;
   int token;
 };
 struct Lists {
@@ -167,43 +171,64 @@ struct Lists {
   uint32_t found;                          // a key
 };
 
-// The weight function of a row, 2^((x - base) c).
+// The weight function of a row, 2^((x - base) c).  A logit's place on the grid
+// is k = floor(512 t + 1/2); adding 1.5 * 2^14 to t leaves it in the low bits of
+// the fp32 sum, and `place` below is that sum as an integer: k plus a constant
+// that is a multiple of 512.  A weight is 2 part + 1 with the part mant * 2^32
+// >> shift: the cut loses half a unit of the part on average and the 1 brings it
+// back, so the sum of many small weights does not drift.
+// These run once or twice per logit and are bound by the integer pipe, at half
+// the rate of fp32: hence the choice of constants folded together, the table with
+// both forms, and no clamping: for logits below the support (-inf, NaN) the
+// numbers mean nothing, and the caller drops them.
 struct RowWeight {
   float base, ch, cl;  // c = ch + cl
-  float least;         // the support's end: smaller logits are taken for it
-  int top;             // exponent of the largest weight, + down
+  float least;         // the support's end
+  uint32_t top;        // the shift of a part is top - (place >> 9)
 };
 struct Weight {
-  uint32_t mant;  // [2^31, 2^32)
-  int shift;      // the weight is (mant << 31) >> shift
+  uint32_t mant;   // [2^31 2^(-1/1024), 2^32)
+  uint32_t shift;  // below 2 + 22 + 42; the largest logit's is down + 2
 };
-// t of a logit as k/512 + *g: adding 1.5 * 2^14 rounds it to 9 fraction bits.
-__device__ __forceinline__ int grid_of(const RowWeight& rw, float x, float* g) {
-  const float d = fmaxf(x, rw.least) - rw.base;  // (NaN: least)
+__device__ __forceinline__ uint32_t place_of(const RowWeight& rw, float x, float* g) {
+  const float d = x - rw.base;
   const float k = fmaf(d, rw.ch, 24576.f);
   *g = fmaf(d, rw.cl, fmaf(d, rw.ch, 24576.f - k));
-  return (int)(__float_as_uint(k) - __float_as_uint(24576.f));
+  return __float_as_uint(k);
 }
-__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x, int* at, float* g) {
-  const int k = *at = grid_of(rw, x, g);
-  const float r = *g * fmaf(*g, 0.2402265070f, 0.6931471806f);  // 2^g - 1
-  Weight w;
-  const uint32_t t = table[k & (kGrid - 1)];
-  // t r, rounded to an integer by adding 1.5 * 2^23 (|t r| < 2^22); t as fp32
-  // by its bits: 2^31 <= t < 2^32
-  const float tf = __uint_as_float((t >> 8) + 0x4E800000u);
-  w.mant = t + (__float_as_uint(fmaf(tf, r, 12582912.f)) - 0x4B400000u);
-  w.shift = rw.top - (k >> kGridBits);  // at most down + 41 <= 63
-  return w;
-}
-__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint32_t* table, float x) {
-  int at;
+__device__ __forceinline__ uint32_t place_of(const RowWeight& rw, float x) { return __float_as_uint(fmaf(x - rw.base, rw.ch, 24576.f)); }
+__device__ __forceinline__ Weight weight_of(const RowWeight& rw, const uint2* table, float x, uint32_t* place) {
   float g;
-  return weight_of(rw, table, x, &at, &g);
+  const uint32_t k = *place = place_of(rw, x, &g);
+  const float r = g * fmaf(g, 0.2402265070f, 0.6931471806f);  // 2^g - 1
+  const uint2 t = table[k & (kGrid - 1)];
+  // t r, rounded to an integer by adding 1.5 * 2^23 (|t r| < 2^22)
+  return Weight{t.x + __float_as_uint(fmaf(__uint_as_float(t.y), r, 12582912.f)), rw.top - (k >> kGridBits)};
 }
-// The lowest bit is always set: like a rounding, unlike the cut alone, that
-// is right on average, so the sum of many small weights does not drift.
-__device__ __forceinline__ u64 fixed(const Weight& w) { return (((u64)w.mant << 31) >> w.shift) | 1; }
+__device__ __forceinline__ u64 part_of(const Weight& w) {
+  u64 v;  // (shifts beyond 63 give 0)
+  asm("shr.u64 %0, %1, %2;" : "=l"(v) : "l"((u64)w.mant << 32), "r"(w.shift));
+  return v;
+}
+// The weight as fp32, off by two roundings.
+__device__ __forceinline__ float weight_fp32(const RowWeight& rw, const uint2* table, float x) {
+  float g;
+  const uint32_t k = place_of(rw, x, &g);
+  const float t = __uint_as_float(table[k & (kGrid - 1)].y);
+  const float v = fmaf(t, g * fmaf(g, 0.2402265070f, 0.6931471806f), t);
+  return __uint_as_float(__float_as_uint(v) + ((33u - (rw.top - (k >> kGridBits))) << 23));  // v 2^33 >> shift
+}
+// 1 / v, to nearest or next to it.
+__device__ __forceinline__ float reciprocal(u64 v) {
+  const float hi = (float)v;
+  const float lo = (float)(long long)(v - (u64)hi);
+  const float r = 1.f / hi;
+  return fmaf(r, fmaf(-hi, r, 1.f) - lo * r, r);
+}
+__device__ __forceinline__ u64 fixed(const Weight& w) { return 2 * part_of(w) + 1; }
+__device__ __forceinline__ u64 fixed(const RowWeight& rw, const uint2* table, float x, uint32_t* place) {
+  return fixed(weight_of(rw, table, x, place));
+}
 
 // Order-preserving integer of a float, and back.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -375,7 +400,7 @@ __device__ __forceinline__ void kth_key(const uint32_t* keys, int n, int k, uint
 }
 
 // A bin's word: the logits in it (up to 2^22) and, in the upper 9 bits, the sum
-// of their places 0..15 in the bin, which is right for up to 32 of them.
+// of their places 0..7 in the bin, which is right for up to 73 of them.
 constexpr int kCountBits = 23;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
 // Estimated weight of a bin, in units of the weight of the largest logit's
@@ -383,8 +408,8 @@ constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
 // within it the weight falls by 1 - 2^(-1/64) = 0.010772.
 __device__ __forceinline__ float bin_estimate(uint32_t word, int bin) {
   const float c = (float)(word & kCountMask);
-  const float places = c <= 32.f ? (float)(word >> kCountBits) : 7.5f * c;
-  return fast_exp2((0.5f / kGrid) - (float)bin * 0.015625f) * (c - (2.f * places + c) * (0.010772f / 32.f));
+  const float places = c <= 73.f ? (float)(word >> kCountBits) : 3.5f * c;
+  return fast_exp2((0.5f / kGrid) - (float)bin * 0.015625f) * (c - (2.f * places + c) * (0.010772f / 16.f));
 }
 // (logits, estimate) as one word of an exchange
 __device__ __forceinline__ u64 pack_est(uint32_t n, float e) { return ((u64)n << 32) | __float_as_uint(e); }
@@ -506,7 +531,7 @@ struct Row {
   Shared* s;
   int lo;          // index of the slice's first logit
   float m;         // the largest logit
-  int top_grid;    // its place on the grid
+  uint32_t top_place;  // its place on the grid
   // The thread's largest logit, its group, and the largest of the other groups:
   // what is kept in the end is mostly a few logits, so that hardly a thread has
   // to look at its logits again.
@@ -598,15 +623,18 @@ struct Row {
     constexpr float kHi = (float)kWidth, kLo = (float)(kWidth - (double)kHi);
     const float hi = tau * kHi;
     rw.least = add_up(m, -hi, -(fmaf(tau, kHi, -hi) + tau * kLo));
-    float g;
-    top_grid = grid_of(rw, m, &g);
-    rw.top = (top_grid >> kGridBits) + down;
+    top_place = place_of(rw, m);
+    rw.top = (top_place >> kGridBits) + (uint32_t)down + 2;
   }
-  __device__ __forceinline__ u64 weight(float x) const { return fixed(weight_of(rw, s->table, x)); }
+  // of a logit that may be below the support: as at its end
+  __device__ __forceinline__ u64 weight(float x) const {
+    uint32_t place;
+    return fixed(rw, s->table, fmaxf(x, rw.least), &place);
+  }
   // No logit less than d grid steps below the largest is below this: two steps
   // and the rounding of |t| < 2^13 further down.
   __device__ __forceinline__ float least_of(int d) const {
-    const float t = (float)(top_grid - d - 2) * (1.f / kGrid);
+    const float t = (float)((int)(top_place - kGridZero) - d - 2) * (1.f / kGrid);
     const float x = (t - fabsf(t) * 0x1p-20f) / rw.ch;
     return (x - fabsf(x) * 0x1p-20f) + (rw.base - fabsf(rw.base) * 0x1p-22f);
   }
@@ -747,6 +775,21 @@ struct Border {
   u64 here;
 };
 
+__device__ __forceinline__ void smem_add(uint32_t addr, uint32_t v) {
+  asm volatile("red.shared.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Where x >= base: part onto sum, one onto the bin; without a branch.
+__device__ __forceinline__ void add_where_counted(float x, float base, u64 part, uint32_t bin, uint32_t one, u64& sum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ge.f32 p, %3, %4;\n\t"
+      "@p add.u64 %0, %0, %5;\n\t"
+      "@p red.shared.add.u32 [%1], %2;\n\t}"
+      : "+l"(sum)
+      : "r"(bin), "r"(one), "f"(x), "f"(base), "l"(part)
+      : "memory");
+}
+
 // kWeight false: the top_k-th largest of the logits >= base.  kWeight true: the
 // largest logit from which on the logits >= base hold the share top_p of their
 // weight.  base is inside the support.
@@ -760,28 +803,30 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
   __syncthreads();
   for (int b = threadIdx.x; b < kBins; b += kThreads) f.hist[b] = 0;
   __syncthreads();
-  // the histogram and, for top-p, the exact weight of all
+  // the histogram and, for top-p, the parts of all weights
   u64 all = 0;
+  const uint32_t hist = smem_u32(f.hist);
   row.sl.template own<kResident, 8 / kN>([&](const float(&x)[kN], int, int) {
-    int bin[kN];
-    uint32_t one[kN];
+    uint32_t bin[kN], one[kN];
+    u64 part[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      int k;
-      float g;
-      if (kWeight) {
-        const u64 w = fixed(weight_of(row.rw, row.s->table, x[i], &k, &g));
-        all += x[i] >= base ? w : 0;
-      } else {
-        k = grid_of(row.rw, x[i], &g);
-      }
-      const int d = row.top_grid - k;
-      bin[i] = d >> 3;
-      one[i] = 1u + ((uint32_t)(((d & 7) << 1) + (int)(__float_as_uint(g) >> 31)) << kCountBits);
+      uint32_t k;
+      if (kWeight)
+        part[i] = part_of(weight_of(row.rw, row.s->table, x[i], &k));
+      else
+        k = place_of(row.rw, x[i]);
+      const uint32_t d = row.top_place - k;
+      bin[i] = hist + (d >> 3) * 4;
+      one[i] = ((d << kCountBits) & (7u << kCountBits)) | 1u;
     }
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (x[i] >= base) atomicAdd(f.hist + bin[i], one[i]);
+    for (int i = 0; i < kN; ++i) {
+      if (kWeight)
+        add_where_counted(x[i], base, part[i], bin[i], one[i], all);
+      else if (x[i] >= base)
+        smem_add(bin[i], one[i]);
+    }
   });
   cl.sync();
   // CTA r adds up share r of the bins (from the largest weights down), thread i
@@ -833,7 +878,7 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
   const float e_all = __shfl_sync(0xFFFFFFFFu, lane_e, 31);
   u64 need = (u64)top_k;
   if (kWeight)
-    need = max(share_of(fraction64(top_p), Cluster::warp_sum(cl.four(shares[1]).sum())), 1ull);
+    need = max(share_of(fraction64(top_p), 2 * Cluster::warp_sum(cl.four(shares[1]).sum()) + n_all), 1ull);
   else if (n_all <= (uint32_t)top_k)
     return out;  // the support holds no more
   // the border is where the running estimate (for top-k the running count,
@@ -956,16 +1001,14 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
       u64 w[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        int k;
-        float g;
+        uint32_t k;
         w[i] = 1;
-        if (kWeight) {
-          w[i] = fixed(weight_of(row.rw, row.s->table, x[i], &k, &g));
-          sums[0] += x[i] >= base && row.top_grid - k < c0 ? w[i] : 0;
-        } else {
-          k = grid_of(row.rw, x[i], &g);
-        }
-        d[i] = row.top_grid - k - c0;
+        if (kWeight)
+          w[i] = fixed(row.rw, row.s->table, x[i], &k);
+        else
+          k = place_of(row.rw, x[i]);
+        d[i] = (int)(row.top_place - k) - c0;
+        if (kWeight) sums[0] += x[i] >= base && d[i] < 0 ? w[i] : 0;
       }
 #pragma unroll
       for (int i = 0; i < kN; ++i)
@@ -1005,7 +1048,8 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
       break;
     }
     // the exact sums say by how much the estimate was off
-    const float unit = (float)fixed(Weight{row.s->table[row.top_grid & (kGrid - 1)], row.rw.top - (row.top_grid >> kGridBits)});
+    const uint2 one = row.s->table[row.top_place & (kGrid - 1)];
+    const float unit = (float)fixed(Weight{one.x + kMagicBits, row.rw.top - (row.top_place >> kGridBits)});
     aim = fmaxf(e_c0 + (float)(long long)(need - over) / unit, 0.f);
     over = 0;
   }
@@ -1250,14 +1294,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   }
   if (!drawn) {
-    if (!summed)
+    if (!summed) {
+      uint32_t kept = 0;
       row.reaching(theta, [&](const float(&x)[kN], int) {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          const u64 w = row.weight(x[i]);
-          mine += x[i] >= theta ? w : 0;
+          uint32_t place;
+          const u64 part = part_of(weight_of(row.rw, s.table, x[i], &place));
+          if (x[i] >= theta) {
+            mine += part;
+            ++kept;
+          }
         }
       });
+      mine = 2 * mine + kept;
+    }
     total = draw(row, a, t, theta, mine, chance, greedy && probs);
   }
   if (!probs) return;
@@ -1266,9 +1317,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     for (int i = threadIdx.x; i < sl.n; i += kThreads) probs[i] = row.lo + i == s.token ? 1.f : 0.f;
     return;
   }
-  if (threadIdx.x == 0) s.inv_total = (float)(1.0 / (double)total);
-  __syncthreads();
-  const float inv = s.inv_total;
+  const float inv = reciprocal(total);
   const bool wide = ((reinterpret_cast<uintptr_t>(probs) - 4u * sl.head) & 15u) == 0;  // groups at 16-byte addresses
   const int run_end = sl.run_end();
   sl.template own<kResident, 2>([&](const float(&x)[kN], int i0, int g) {
@@ -1280,8 +1329,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
       for (int i = 0; i < kN; ++i)
         if (x[i] >= theta) {
-          const Weight w = weight_of(row.rw, s.table, x[i]);
-          p[i] = (float)w.mant * __uint_as_float((uint32_t)(127 + 31 - w.shift) << 23) * inv;
+          p[i] = weight_fp32(row.rw, s.table, x[i]) * inv;
         }
     }
     if (wide && i0 >= 0 && i0 + kN <= sl.n) {

@@ -6,8 +6,9 @@ one unit, 2^-(62 - ceil(log2 V)) of the largest; a partial sum and the total it
 is compared with are both off by that much for each of at most V weights, so
 slack = 2^-29 + 2 V 2^-(62 - ceil(log2 V)) / (total / largest).  Rows nearer
 than that are not compared; they have to be few.  probs are fp32 quotients of
-such weights: the weight's conversion, the reciprocal and the product round by
-2^-24 each, so 3 * 2^-24 + slack < 2.5e-7 relative."""
+such weights: a weight's table entry and its product with the rest, the
+reciprocal and the product round by 2^-24 each, so 4 * 2^-24 + slack < 2.5e-7
+relative."""
 import numpy as np
 import pytest
 import torch
