@@ -340,8 +340,9 @@ sv_status mla_kv_append(const void* kv_new, const int32_t* positions, const int3
  *              the same time need their own.
  *   status     device int32, may be NULL; ORed with
  *                SV_DEV_BAD_BOUND    a length outside [0, max_pages_per_req*64]
- *                SV_DEV_BAD_PAGE     an entry outside the pool, or a page given
- *                                    back more often than held (it is free)
+ *                SV_DEV_BAD_PAGE     an entry outside the pool or of a free page,
+ *                                    a page given back more often than held (it
+ *                                    is free then)
  *                SV_DEV_NO_PAGE, SV_DEV_SHARED_PAGE, SV_DEV_BAD_REQUEST
  *              What a bit reports is left undone for that request (fork,
  *              pair) only, as said at each call; the rest is done.
@@ -364,8 +365,8 @@ sv_status mla_kv_append(const void* kv_new, const int32_t* positions, const int3
  *   with an index outside [0, R), a child in use or named before
  *   (SV_DEV_BAD_REQUEST), a parent's length out of range or no page left for
  *   its last rows (SV_DEV_NO_PAGE) leaves the child as it was.  A parent's entry
- *   outside the pool is passed on as it is (SV_DEV_BAD_PAGE), counted nowhere
- *   and copied from nowhere.
+ *   outside the pool, or one that names a free page, is passed on as it is
+ *   (SV_DEV_BAD_PAGE), counted nowhere and copied from nowhere.
  *   Two kernels on `stream` (the second a programmatic dependent launch).
  *
  * kv_pages_resize: request r gets the pages of length new_lens[r] (-1: stays

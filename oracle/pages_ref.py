@@ -97,7 +97,7 @@ def ref_pages_fork(pool, ref_counts, block_table, kv_lens, parents, children):
         for j in range(full):
             p = int(block_table[a, j])
             table[b, j] = p
-            if 0 <= p < P:
+            if 0 <= p < P and ref_counts[p] > 0:
                 refs[p] += 1
             else:
                 status |= BAD_PAGE
@@ -105,7 +105,7 @@ def ref_pages_fork(pool, ref_counts, block_table, kv_lens, parents, children):
             p, q = int(block_table[a, full]), free[asked - 1]
             table[b, full] = q
             refs[q] = 1
-            if 0 <= p < P:
+            if 0 <= p < P and ref_counts[p] > 0:
                 pool[:, q, :tail] = pool[:, p, :tail]
             else:
                 status |= BAD_PAGE

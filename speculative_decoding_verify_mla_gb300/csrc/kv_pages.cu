@@ -387,7 +387,7 @@ struct ForkArgs {
   const int32_t *ref_in, *table_in, *lens_in, *parents, *children;
   int32_t *ref_out, *table_out, *lens_out, *status;
   int *claim, *prefix, *list;  // workspace: the first fork onto a child; tails before fork i; free pages
-  int4* moves;                 // workspace: tail page, its copy, rows (0: nothing to copy), length (-1: not done)
+  int4* moves;                 // workspace: tail page, its copy (-1: none), rows (0: nothing to copy), length (-1: not done)
   int P, R, mp, n;
 };
 
@@ -412,6 +412,12 @@ __device__ __forceinline__ Fork read_fork(const ForkArgs& a, int i, bool tell) {
     if (tell) report(a.status, SV_DEV_BAD_BOUND);
   }
   return f;
+}
+
+// Whether an entry of a parent names a page in use (counts from 1 on only grow
+// until the new pages get theirs).
+__device__ __forceinline__ bool in_use(const ForkArgs& a, int p) {
+  return p >= 0 && p < a.P && __ldcg(a.ref_out + p) > 0;
 }
 
 __global__ void __launch_bounds__(kMetaThreads) fork_kernel(const ForkArgs a) {
@@ -452,48 +458,41 @@ __global__ void __launch_bounds__(kMetaThreads) fork_kernel(const ForkArgs a) {
   group_sync(g);
   for (int i = tid >> 5; i < a.n; i += threads >> 5) {
     const Fork f = read_fork(a, i, lane == 0);
-    const int full = f.len / SV_PAGE_SIZE, tail = f.len % SV_PAGE_SIZE;
-    bool done = f.valid;
-    int fresh = -1;
-    if (done && tail != 0) {
-      const int at = __ldcg(a.prefix + i);
-      done = at < found;
-      if (done)
-        fresh = __ldcg(a.list + at);
-      else if (lane == 0)
-        report(a.status, SV_DEV_NO_PAGE);
-    }
+    const int full = f.len / SV_PAGE_SIZE, tail = f.len % SV_PAGE_SIZE, entries = f.valid ? full + (tail != 0) : 0;
+    const int32_t* from = a.table_in + (long long)(f.valid ? f.parent : 0) * a.mp;
+    // the parent's first 32 entries and their counts beside the new page's number
+    const int p0 = lane < entries ? from[lane] : -1;
+    const int at = f.valid && tail != 0 ? __ldcg(a.prefix + i) : -1;
+    const bool used0 = in_use(a, p0);
+    const int fresh = at >= 0 && at < found ? __ldcg(a.list + at) : -1;
+    const bool done = f.valid && at < found;
+    if (f.valid && !done && lane == 0) report(a.status, SV_DEV_NO_PAGE);
     int4 move = make_int4(-1, -1, 0, done ? f.len : -1);
     if (done) {
-      const int32_t* from = a.table_in + (long long)f.parent * a.mp;
       int32_t* to = a.table_out + (long long)f.child * a.mp;
-      for (int j = lane; j < full; j += 32) {
-        const int p = from[j];
-        to[j] = p;
-        if (p >= 0 && p < a.P)
-          atomicAdd(a.ref_out + p, 1);
-        else
-          report(a.status, SV_DEV_BAD_PAGE);
-      }
-      if (lane == 0 && tail != 0) {
-        const int p = from[full];
-        to[full] = fresh;
-        a.ref_out[fresh] = 1;
-        if (p >= 0 && p < a.P)
-          move = make_int4(p, fresh, tail, f.len);
-        else
-          report(a.status, SV_DEV_BAD_PAGE);
+      for (int j = lane; j < entries; j += 32) {
+        const int p = j < 32 ? p0 : from[j];
+        const bool used = j < 32 ? used0 : in_use(a, p);
+        if (!used) report(a.status, SV_DEV_BAD_PAGE);
+        if (j < full) {
+          to[j] = p;
+          if (used) atomicAdd(a.ref_out + p, 1);
+        } else {
+          to[full] = fresh;
+          move = used ? make_int4(p, fresh, tail, f.len) : make_int4(-1, fresh, 0, f.len);
+        }
       }
     }
-    __syncwarp();
-    if (lane == 0) a.moves[i] = move;
+    if (lane == (done && tail != 0 ? full % 32 : 0)) a.moves[i] = move;
   }
-  // the children's lengths last: until here every warp looks at the lengths
-  // as they were before the call, also when they are updated in place
+  // the children's lengths and the new pages' counts last: until here every warp
+  // sees the lengths, and which pages are free, as they were before the call,
+  // also when they are updated in place
   group_sync(g);
   for (int i = tid; i < a.n; i += threads) {
-    const int len = __ldcg(&a.moves[i].w);
-    if (len >= 0) a.lens_out[__ldg(a.children + i)] = len;
+    const int4 m = __ldcg(a.moves + i);
+    if (m.w >= 0) a.lens_out[__ldg(a.children + i)] = m.w;
+    if (m.y >= 0) a.ref_out[m.y] = 1;
   }
 }
 

@@ -166,6 +166,26 @@ def test_fork_bad_data(sv, in_place):
         check((kv, *got, st), (*want[:4], [want[4]]))
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("width", [16, 1024])
+def test_fork_of_free_pages(sv, in_place, width):
+    """Parents whose entries name pages with the count 0, full ones and the last:
+    such a page may be handed out in the same call, so it is not copied from and
+    its count stays that of its new holder."""
+    refs, lens = np.zeros(12, np.int32), np.array([150, 130, 70, 0, 0, 0, 0, 0], np.int32)
+    table = np.full((8, 3), -1, np.int32)
+    table[0], table[1], table[2, :2] = [1, 5, 0], [2, 6, 7], [8, 1]   # 0, 1 and 2 are free
+    refs[[5, 6, 7, 8]] = 1
+    parents, children = [0, 1, 2, 0, 1], [3, 4, 5, 6, 7]
+    pool = make_pool(np.random.default_rng(3), 2, 12, width)
+    want = oracle.ref_pages_fork(pool, refs, table, lens, parents, children)
+    assert want[4] == sv.SV_DEV_BAD_PAGE
+    a, b, c, st, kv = i32(refs), i32(table), i32(lens), i32([0]), dev(pool)
+    outs = dict(ref_counts_out=a, block_table_out=b, kv_lens_out=c) if in_place else {}
+    got = sv.kv_pages_fork(kv, a, b, c, i32(parents), i32(children), status=st, **outs)
+    check((kv, *got, st), (*want[:4], [want[4]]))
+
+
 @pytest.mark.parametrize("P,R,mp,L,width", [(1, 1, 1, 1, 16), (7, 3, 2, 2, 512), (300, 9, 24, 2, 1024), (20000, 64, 100, 1, 16),
                                             (70001, 130, 300, 1, 16), (140000, 33, 40, 1, 16)])
 @pytest.mark.parametrize("in_place", [False, True])
