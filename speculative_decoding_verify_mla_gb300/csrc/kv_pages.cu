@@ -16,9 +16,13 @@
 // other, and a cluster barrier between them costs far less than a launch.
 // Ranking is a prefix sum over warp ballots; the CTAs' totals meet in
 // distributed shared memory.  What bounds it is latency (a few dependent
-// round trips to L2), not bytes.  The pages themselves move in a second
-// kernel over the whole GPU, a programmatic dependent launch, bound by HBM:
-// two bytes of traffic per byte moved.
+// round trips to L2), not bytes: 7 us for eight requests over 256 pages, 16 us
+// for 256 requests of up to 30000 positions over 65536 pages.  The pages
+// themselves move in a second kernel over the whole GPU, a programmatic
+// dependent launch, bound by HBM, two bytes of traffic per byte moved: the tails
+// of 64 forks in 24 layers, 101 MB, 20.5 us with the bookkeeping; half of 1024
+// pages in eight layers, 248 MB, 48 us.  (Moving them in the bookkeeping kernel
+// saves a launch, but a CTA moves little: 3 tails of a layer 8.0 -> 13.8 us.)
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -35,8 +39,12 @@ static_assert(kMetaWarps == 32, "the scans below add up 32 warps, and one warp p
 constexpr int kItems = 8;                            // pages per thread and tile
 constexpr int kTile = kMetaThreads * kItems;         // pages per CTA and tile
 constexpr int kClusterMax = 8;
-// Pools and tables of at most this many words together take one CTA.
-constexpr long long kOneCtaWords = 16384;
+// Pools and tables of at most this many words together take one CTA, whose
+// barriers are cheap, larger ones eight.  One against eight, in us: resize of
+// 448 words 7.0 / 8.8, 7168 words 10.3 / 11.0, 14336 words 13.9 / 11.3, 196608
+// words 48 / 14; compact (bookkeeping and small moves) 256 pages 6.2 / 8.4, 8192
+// pages 14.7 / 16.7, 12288 pages 20.3 / 19.8.
+constexpr long long kOneCtaWords = 8192;
 constexpr int kAhead = 8;                            // loads of a thread under way at once
 constexpr int kCopyThreads = 256;
 constexpr int kChunkWords = 8;                       // 16-byte words of a chunk per thread
@@ -709,7 +717,7 @@ cudaError_t launch_meta(void (*kernel)(Args), const Args& a, long long words, cu
 }
 
 // A chunk of 32 KB per CTA: 256 pages of 64 KB in 24 layers (805 MB of traffic)
-// take 121 us so, 6.65 TB/s as a plain device copy does, against 131 us for
+// take 119 us so, 6.77 TB/s as a plain device copy does, against 131 us for
 // 1216 resident CTAs that loop over the chunks and 123-135 us for rings of
 // bulk copies.  Chunks of 16 KB do the same here, but lose 2 us where every
 // CTA first reads what it is to move (64 tails in 24 layers: 22.7 against 20.7

@@ -38,7 +38,7 @@
 //    is inside, whose weights every CTA then adds up.
 //  * Where the window holds too many (ties): quartering of the logits' bits.
 // What bounds it: with many rows HBM (512 rows of 163840 fp32 logits under a
-// min-p: 64 us, 5.2 TB/s), or under top-p instruction issue (about 45
+// min-p: 61 us, 5.5 TB/s), or under top-p instruction issue (about 45
 // instructions a logit, 32 of them its weight); with few rows the latency of
 // the meetings (one row under top-k 50, top-p 0.9: 9.5 us).
 #include <cuda_bf16.h>
@@ -144,7 +144,6 @@ struct SampleArgs {
   double ln_min_p_all;  // ln(min_p_all), 0 above 1
   long long row_stride;
   int V, slice;      // slice: logits per CTA, a multiple of 8
-  int rows, ahead;   // row t + ahead is fetched into L2 early (0: none)
   int down;          // the largest weight is mant << 31 >> down (mant < 2^32): V of them stay below 2^63
   int32_t* tokens;
   float* probs;
@@ -544,16 +543,6 @@ __device__ __forceinline__ bool wait_piece(uint32_t bar) {
       return false;
     }
   return true;
-}
-
-// The slice `away` elements further on, from HBM into L2: a hint.
-template <typename T>
-__device__ __forceinline__ void prefetch_row(const Slice<T>& sl, long long away) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(sl.src + away);
-  const uintptr_t p0 = (p + 15) & ~(uintptr_t)15, p1 = (p + (size_t)sl.n * sizeof(T)) & ~(uintptr_t)15;
-  constexpr uintptr_t kPart = 16384;
-  for (uintptr_t at = p0 + threadIdx.x * kPart; at < p1; at += kThreads * kPart)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"((uint32_t)min(kPart, p1 - at)) : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -1256,8 +1245,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (!row.stage() && a.status) atomicOr(a.status, SV_DEV_TIMEOUT);
   }
   row.find_top();
-  // rows that are not on the GPU yet start on their way into L2
-  if (!kResident && a.ahead > 0 && t + a.ahead < a.rows) prefetch_row<T>(sl, a.ahead * a.row_stride);
 
   const bool greedy = tau < kColdest;
   if (greedy) {
@@ -1503,8 +1490,6 @@ extern "C" sv_status sample_tokens(const void* logits, int logits_type, int T, i
   const bool floored = min_p || min_p_all > 0.f || (!temperature && temperature_all < kColdest);
   const Shape sh = row_shape(T, V, elem, filters ? (top_p || top_p_all < 1.f) && !small_k : !floored);
   a.slice = sh.slice;
-  a.rows = T;
-  a.ahead = sh.ctas == 1 && T > 2 * kSms ? 2 * kSms : 0;
   a.down = 0;
   while ((1 << a.down) < V) ++a.down;  // V <= 2^down: V (2^63 >> down) <= 2^63
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
