@@ -251,6 +251,30 @@ def test_empty_calls(sv):
         check(got[0:1] + got[2:], ([1, 2, 0, 0], [0, -1, 1, -1], [2]))
 
 
+def test_pools_past_32_bits(sv):
+    """Pages beyond 4 GB of a layer and beyond 2^32 bytes of the pool: copied,
+    forked from and moved, in both layers; nothing else changes."""
+    P, L = 36000, 2
+    pool = torch.zeros((L, P, 64, 512), dtype=torch.bfloat16, device=DEV)   # 2.4 GB a layer
+    pool.view(L, P, -1)[:, :, 0] = torch.arange(P, device=DEV).remainder(251).bfloat16() + torch.tensor([[0.0], [256.0]], device=DEV).bfloat16()
+    first = pool.view(L, P, -1)[:, :, 0].clone()
+    page = torch.randn((L, 64, 512), device=DEV).bfloat16()
+    pool[:, P - 1], pool[:, P - 2] = page, 2 * page
+    sv.kv_pages_copy(pool, pool, i32([P - 1]), i32([P - 3]))
+    assert torch.equal(pool[:, P - 3], page)
+    refs = np.zeros(P, np.int32)
+    refs[[0, P - 1, P - 2]] = 1
+    table, lens = np.array([[0, P - 1], [P - 2, -1], [-1, -1]], np.int32), np.array([128, 30, 0], np.int32)
+    state = sv.kv_pages_fork(pool, i32(refs), i32(table), i32(lens), i32([1]), i32([2]))   # a tail into page 1
+    assert state[1].tolist() == [[0, P - 1], [P - 2, -1], [1, -1]] and state[2].tolist() == [128, 30, 30]
+    assert torch.equal(pool[:, 1, :30], 2 * page[:, :30]) and torch.equal(pool[:, 1, 30:], torch.zeros_like(page[:, 30:]))
+    refs, table, page_map, live = sv.kv_pages_compact(pool, *state)
+    assert live.item() == 4 and table.tolist() == [[0, 3], [2, -1], [1, -1]] and page_map[[P - 2, P - 1]].tolist() == [2, 3]
+    assert torch.equal(pool[:, 3], page) and torch.equal(pool[:, 2], 2 * page)
+    same = pool.view(L, P, -1)[:, 4:P - 3, 0]
+    assert torch.equal(same, first[:, 4:P - 3])
+
+
 def test_tables_without_entries(sv):
     """Requests that can hold nothing: a length other than 0 is out of range."""
     refs, table, lens = i32(np.zeros(5)), i32(np.zeros((3, 0))), i32(np.zeros(3))

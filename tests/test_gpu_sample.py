@@ -309,6 +309,33 @@ def test_repeated_calls_agree(sv):
             assert torch.equal(g[0], want[i % 4][0]) and torch.equal(g[1], want[i % 4][1])
 
 
+def test_offsets_past_32_bits(sv):
+    """Rows and distributions that begin beyond 2^31 elements, dense and by a
+    stride, give what the same row gives alone."""
+    T, V = 520, 1 << 22
+    x = torch.empty((T, V), dtype=torch.bfloat16, device=DEV).normal_(std=2.0, generator=torch.Generator(DEV).manual_seed(1))
+    u = torch.rand(T, device=DEV, generator=torch.Generator(DEV).manual_seed(2))
+    for s in (dict(top_k=50), dict(min_p=0.2)):
+        tok, p = sv.sample_tokens(x, u, return_probs=True, **s)
+        for t in (0, T - 2, T - 1):
+            one, q = sv.sample_tokens(x[t:t + 1], u[t:t + 1], return_probs=True, **s)
+            assert int(one) == int(tok[t]) and torch.equal(q[0], p[t])
+        del p
+    far = x.view(-1)[7:].as_strided((2, 32003), (2_170_000_001, 1))
+    assert torch.equal(sv.sample_tokens(far, u[:2], top_p=0.9), torch.cat([sv.sample_tokens(far[i:i + 1], u[i:i + 1], top_p=0.9) for i in (0, 1)]))
+
+
+def test_many_small_rows(sv):
+    """More rows than a grid dimension of 16 bits holds."""
+    x = torch.randn((70001, 5), device=DEV, generator=torch.Generator(DEV).manual_seed(3))
+    u = torch.rand(70001, device=DEV, generator=torch.Generator(DEV).manual_seed(4))
+    want = x.argmax(1).int()
+    assert torch.equal(sv.sample_tokens(x, u, temperature=0.0), want)
+    tok, p = sv.sample_tokens(x, u, top_k=1, top_p=0.5, return_probs=True)
+    hot = torch.nn.functional.one_hot(want.long(), 5).double()
+    assert torch.equal(tok, want) and float((p.double() - hot).abs().max()) <= REL and int((p > 0).sum()) == 70001  # (a quotient of 1)
+
+
 def test_top_k_past_32_bits(sv):
     x, u = dev(logits(np.random.default_rng(23), 3, 900)), torch.rand(3, device=DEV)
     for k, same in ((2 ** 32 + 5, 0), (2 ** 31, 0), (-2 ** 32 + 5, 0), (899, 899)):
