@@ -167,6 +167,8 @@ struct Lists {
   uint32_t hist[kBins];                    // see bin_estimate
   u64 sums[2];
   int count;                               // candidates found here
+  int c0, c1;                              // grid steps of a window
+  uint32_t before;                         // logits in the bins before it
   uint32_t found, above;                   // keys
   int between;
 };
@@ -818,6 +820,124 @@ __device__ __forceinline__ void add_where_counted(float x, float base, u64 part,
       : "memory");
 }
 
+// Where the border is looked up: a window of grid steps [f.c0, f.c1] below the
+// largest logit.  aim: the estimate that it has to reach (top-p; top_k else); where
+// that is beyond the last logit the border is looked up there.  slot: the sums of the histogram's parts, in bin order; per: bins
+// of a lane in a slot, own: of a CTA's share.  One warp.  Returns the estimate
+// before the window.
+template <bool kWeight>
+__device__ __forceinline__ float find_window(Lists& f, const Cluster::Four& slot, int own, int per, uint32_t top_k, float aim) {
+  const int lane = threadIdx.x & 31;
+  auto reached = [&](uint32_t n, float e) { return kWeight ? e >= aim : n >= top_k; };
+  uint32_t n = 0;
+  float e = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    n += (uint32_t)(slot.v[i] >> 32);
+    e += __uint_as_float((uint32_t)slot.v[i]);
+  }
+  // the first slot where the aim is reached, else the last in use
+  n = scan_add(n) - n;
+  e = scan_add(e) - e;
+  int used = -1;
+  bool hit = false;
+  uint32_t n_at = 0;
+  float e_at = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t slot_n = (uint32_t)(slot.v[i] >> 32);
+    const float slot_e = __uint_as_float((uint32_t)slot.v[i]);
+    if (slot_n > 0 && !hit) {
+      used = i;
+      n_at = n;
+      e_at = e;
+      hit = reached(n + slot_n, e + slot_e);
+    }
+    n += slot_n;
+    e += slot_e;
+  }
+  unsigned who = __ballot_sync(0xFFFFFFFFu, hit);
+  int l0 = who ? __ffs(who) - 1 : 31 - __clz(__ballot_sync(0xFFFFFFFFu, used >= 0));
+  const int at = 4 * l0 + __shfl_sync(0xFFFFFFFFu, used, l0);
+  n = __shfl_sync(0xFFFFFFFFu, n_at, l0);
+  e = __shfl_sync(0xFFFFFFFFu, e_at, l0);
+  const int first = ((at % kWarps) * 32 + lane) * per;  // the lane's bins of the slot, in its share
+  const int bin0 = at / kWarps * own + first, bins = min(per, own - first);
+  uint32_t n_here = 0;
+  float e_here = 0.f;
+  for (int i = 0; i < bins; ++i) {
+    const uint32_t word = f.hist[bin0 + i];
+    n_here += word & kCountMask;
+    e_here += bin_estimate(word, bin0 + i);
+  }
+  const uint32_t n_first = n + scan_add(n_here) - n_here;
+  const float e_first = e + (scan_add(e_here) - e_here);
+  // the first of its bins where the aim is reached: logits and weight before it,
+  // in it; where rounding keeps all of them below the aim, the last bin in use
+  int cross = -1, last = -1, in_cross = 0;
+  uint32_t cross_n = 0;
+  float cross_e = 0.f, cross_w = 0.f;
+  n = n_first;
+  e = e_first;
+  for (int i = 0; i < bins; ++i) {
+    const uint32_t word = f.hist[bin0 + i], c = word & kCountMask;
+    const float est = bin_estimate(word, bin0 + i);
+    if (c && cross < 0) {
+      last = bin0 + i;
+      if (reached(n + c, e + est)) cross = last;
+      cross_n = n;
+      cross_e = e;
+      cross_w = est;
+      in_cross = (int)c;
+    }
+    n += c;
+    e += est;
+  }
+  who = __ballot_sync(0xFFFFFFFFu, cross >= 0);
+  l0 = who ? __ffs(who) - 1 : 31 - __clz(__ballot_sync(0xFFFFFFFFu, last >= 0));
+  cross = __shfl_sync(0xFFFFFFFFu, last, l0);
+  cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l0);
+  cross_e = __shfl_sync(0xFFFFFFFFu, cross_e, l0);
+  cross_w = __shfl_sync(0xFFFFFFFFu, cross_w, l0);
+  in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l0);
+  // For top-k the window is the bin; for top-p, in a bin of few logits, the bins
+  // around it with kMargin logits on both sides, in a bin of many the steps
+  // around the place in it where the estimate puts the border.
+  int c0 = 8 * cross, c1 = 8 * cross + 7;
+  float e_c0 = cross_e;
+  if (kWeight && in_cross > kMargin) {
+    const float place = fminf(fmaxf((aim - cross_e) / cross_w, 0.f), 1.f) * 8.f;
+    const float reach = 8.f * kMargin / (float)in_cross + 0.25f;
+    c0 += (int)floorf(place - reach);
+    c1 = 8 * cross + (int)ceilf(place + reach);
+    e_c0 += cross_w * (float)(c0 - 8 * cross) * 0.125f;
+  } else if (kWeight) {
+    n = n_first;
+    e = e_first;
+    for (int i = 0; i < bins; ++i) {
+      const int bin = bin0 + i;
+      const uint32_t word = f.hist[bin], c = word & kCountMask;
+      if (bin < cross && cross_n - n <= kMargin) {
+        c0 = min(c0, 8 * bin);
+        e_c0 = fminf(e_c0, e);
+      }
+      if (bin > cross && n + c <= cross_n + in_cross + kMargin) c1 = max(c1, 8 * bin + 7);
+      n += c;
+      e += bin_estimate(word, bin);
+    }
+    c0 = __reduce_min_sync(0xFFFFFFFFu, c0);
+    c1 = __reduce_max_sync(0xFFFFFFFFu, c1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) e_c0 = fminf(e_c0, __shfl_xor_sync(0xFFFFFFFFu, e_c0, o));
+  }
+  if (lane == 0) {
+    f.c0 = c0;
+    f.c1 = c1;
+    f.before = cross_n;
+  }
+  return e_c0;
+}
+
 // kWeight false: the top_k-th largest of the logits >= base.  kWeight true: the
 // largest logit from which on the logits >= base hold the share top_p of their
 // weight.  base is inside the support.
@@ -826,7 +946,6 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
   constexpr int kN = R::kN;
   constexpr bool kResident = R::kInShared;
   Cluster& cl = row.cl;
-  const int lane = threadIdx.x & 31;
   Border out{-INFINITY, false, 0};
   __syncthreads();
   for (int b = threadIdx.x; b < kBins; b += kThreads) f.hist[b] = 0;
@@ -863,7 +982,6 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
   // that every CTA has the row's histogram.
   const int own = kBins / (int)cl.size;
   const int per = (own + kThreads - 1) / kThreads;
-  constexpr int kPer = (kBins + kThreads - 1) / kThreads;
   u64 v[2] = {0, Cluster::warp_sum(all)};
   {
     uint32_t n = 0;
@@ -891,136 +1009,38 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
     v[0] = pack_est(n, e);
   }
   const u64(*const shares)[kSlots] = cl.leave(v);
-  // every warp finds the border's bin by itself
   const Cluster::Four slot = cl.four(shares[0]);
-  uint32_t slot_n[4], lane_n = 0;
-  float slot_e[4], lane_e = 0.f;
+  uint32_t n_all = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lane_n += slot_n[i] = (uint32_t)(slot.v[i] >> 32);
-    lane_e += slot_e[i] = __uint_as_float((uint32_t)slot.v[i]);
-  }
-  lane_n = scan_add(lane_n);
-  lane_e = scan_add(lane_e);
-  const uint32_t n_all = __shfl_sync(0xFFFFFFFFu, lane_n, 31);
-  const float e_all = __shfl_sync(0xFFFFFFFFu, lane_e, 31);
+  for (int i = 0; i < 4; ++i) n_all += (uint32_t)(slot.v[i] >> 32);
+  n_all = __reduce_add_sync(0xFFFFFFFFu, n_all);
   u64 need = (u64)top_k;
   if (kWeight)
     need = max(share_of(fraction64(top_p), 2 * Cluster::warp_sum(cl.four(shares[1]).sum()) + n_all), 1ull);
   else if (n_all <= (uint32_t)top_k)
     return out;  // the support holds no more
-  // the border is where the running estimate (for top-k the running count,
-  // which is exact) reaches the aim
-  float aim = kWeight ? fmaxf(top_p, 0.f) * e_all : 0.f;
-  auto reached = [&](uint32_t n, float e) { return kWeight ? e >= aim : n >= (uint32_t)top_k; };
+  // The border is where the running estimate (for top-k the running count,
+  // which is exact) reaches the aim.  One warp looks up where.
+  float aim = 0.f, e_c0 = 0.f;
+  if (kWeight && threadIdx.x < 32) {
+    float e_all = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e_all += __uint_as_float((uint32_t)slot.v[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) e_all += __shfl_xor_sync(0xFFFFFFFFu, e_all, o);
+    aim = fmaxf(top_p, 0.f) * e_all;
+  }
   // what the quartering below searches: [low, high], `over` above it
   float low = base, high = row.m;
   u64 over = 0;
   bool listed = false;  // what is in it is in f.cand
   for (int attempt = 0; attempt < kTries; ++attempt) {
-    // the first slot, then the first of its bins, where the aim is reached
-    const uint32_t up_n = __shfl_up_sync(0xFFFFFFFFu, lane_n, 1);
-    const float up_e = __shfl_up_sync(0xFFFFFFFFu, lane_e, 1);
-    uint32_t n = lane > 0 ? up_n : 0;  // before slot 4 lane + q
-    float e = lane > 0 ? up_e : 0.f;
-    int q = -1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (q < 0) {
-        if (slot_n[i] > 0 && reached(n + slot_n[i], e + slot_e[i])) {
-          q = i;
-        } else {
-          n += slot_n[i];
-          e += slot_e[i];
-        }
-      }
-    unsigned who = __ballot_sync(0xFFFFFFFFu, q >= 0);
-    if (who == 0) break;  // (rounding, or a second guess) beyond the last logit
-    int l0 = __ffs(who) - 1;
-    const int at = 4 * l0 + __shfl_sync(0xFFFFFFFFu, q, l0);
-    n = __shfl_sync(0xFFFFFFFFu, n, l0);
-    e = __shfl_sync(0xFFFFFFFFu, e, l0);
-    const int owner = at / kWarps;
-    const int first = ((at % kWarps) * 32 + lane) * per;  // the lane's bins of the slot, in its share
-    const int bin0 = owner * own + first;
-    uint32_t word[kPer], n_here = 0;
-    float est[kPer], e_here = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      word[i] = i < per && first + i < own ? f.hist[bin0 + i] : 0;
-      est[i] = bin_estimate(word[i], bin0 + i);
-      n_here += word[i] & kCountMask;
-      e_here += est[i];
-    }
-    const uint32_t n_first = n + scan_add(n_here) - n_here;
-    const float e_first = e + (scan_add(e_here) - e_here);
-    // that bin: logits and weight before it, in it; where rounding keeps all of
-    // them below the aim, the last bin in use
-    int cross = -1, last = -1, in_cross = 0;
-    uint32_t cross_n = 0;
-    float cross_e = 0.f, cross_w = 0.f;
-    n = n_first;
-    e = e_first;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t c = word[i] & kCountMask;
-      const bool take = c && cross < 0 && reached(n + c, e + est[i]);
-      if (take) cross = bin0 + i;
-      if (c && (take || cross < 0)) {
-        last = bin0 + i;
-        cross_n = n;
-        cross_e = e;
-        cross_w = est[i];
-        in_cross = (int)c;
-      }
-      n += c;
-      e += est[i];
-    }
-    who = __ballot_sync(0xFFFFFFFFu, cross >= 0);
-    l0 = who ? __ffs(who) - 1 : 31 - __clz(__ballot_sync(0xFFFFFFFFu, last >= 0));
-    cross = __shfl_sync(0xFFFFFFFFu, last, l0);
-    cross_n = __shfl_sync(0xFFFFFFFFu, cross_n, l0);
-    cross_e = __shfl_sync(0xFFFFFFFFu, cross_e, l0);
-    cross_w = __shfl_sync(0xFFFFFFFFu, cross_w, l0);
-    in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l0);
-    // The window of grid steps [c0, c1] in which the border is looked up: for
-    // top-k the bin; for top-p, in a bin of few logits, the bins around it with
-    // kMargin logits on both sides, in a bin of many the steps around the place
-    // in it where the estimate puts the border.
-    int c0 = 8 * cross, c1 = 8 * cross + 7;
-    float e_c0 = cross_e;  // the estimate before the window
-    if (kWeight && in_cross > kMargin) {
-      const float place = fminf(fmaxf((aim - cross_e) / cross_w, 0.f), 1.f) * 8.f;
-      const float reach = 8.f * kMargin / (float)in_cross + 0.25f;
-      c0 += (int)floorf(place - reach);
-      c1 = 8 * cross + (int)ceilf(place + reach);
-      e_c0 += cross_w * (float)(c0 - 8 * cross) * 0.125f;
-    } else if (kWeight) {
-      n = n_first;
-      e = e_first;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int bin = bin0 + i;
-        const uint32_t c = word[i] & kCountMask;
-        if (i < per && first + i < own) {
-          if (bin < cross && cross_n - n <= kMargin) {
-            c0 = min(c0, 8 * bin);
-            e_c0 = fminf(e_c0, e);
-          }
-          if (bin > cross && n + c <= cross_n + in_cross + kMargin) c1 = max(c1, 8 * bin + 7);
-        }
-        n += c;
-        e += est[i];
-      }
-      c0 = __reduce_min_sync(0xFFFFFFFFu, c0);
-      c1 = __reduce_max_sync(0xFFFFFFFFu, c1);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) e_c0 = fminf(e_c0, __shfl_xor_sync(0xFFFFFFFFu, e_c0, o));
-    }
-
-    // the exact weight above the window, and what is in the window
+    if (threadIdx.x < 32) e_c0 = find_window<kWeight>(f, slot, own, per, (uint32_t)top_k, aim);
     if (threadIdx.x == 0) f.count = 0;
     __syncthreads();
+    const int c0 = f.c0, c1 = f.c1;
+    const uint32_t cross_n = f.before;
+    // the exact weight above the window, and what is in the window
     u64 sums[3] = {0, 0, 0};  // weight above the window; logits and weight in it
     uint32_t key_min = 0xFFFFFFFFu, key_max = 0;
     const unsigned width = (unsigned)(c1 - c0);
