@@ -74,7 +74,7 @@ constexpr int kPublished = 512;  // largest logits published for a small top-k
 constexpr int kList = 512;       // candidates that one CTA ranks, one per thread
 constexpr int kBins = 2592;      // bins of 1/64 octave of weight: 40.5 octaves, a multiple of 8 shares
 constexpr int kMargin = 64;      // logits on both sides of the place where top-p's border is expected
-constexpr int kTries = 2;        // guesses of it before the quartering
+constexpr int kTries = 3;        // guesses of it before the quartering
 
 // round(2^31 2^(j/512)), j = 0..511, by the exponential series: {the integer
 // less kMagicBits, its fp32 as bits}.
@@ -555,6 +555,7 @@ struct Row {
   using V = Vec<T>;
   static constexpr int kN = V::kN;
   static constexpr bool kInShared = kResident;
+  static constexpr int kKeyBits = sizeof(T) == 2 ? 16 : 0;  // of a key: the same in every logit of a sign
   Cluster cl;
   Slice<T> sl;
   RowWeight rw;
@@ -823,10 +824,11 @@ __device__ __forceinline__ void add_where_counted(float x, float base, u64 part,
 // Where the border is looked up: a window of grid steps [f.c0, f.c1] below the
 // largest logit.  aim: the estimate that it has to reach (top-p; top_k else); where
 // that is beyond the last logit the border is looked up there.  slot: the sums of the histogram's parts, in bin order; per: bins
-// of a lane in a slot, own: of a CTA's share.  One warp.  Returns the estimate
-// before the window.
+// of a lane in a slot, own: of a CTA's share; spread: whether logits are spread
+// over the places of a bin.  One warp.  Returns the estimates before the window
+// and after it.
 template <bool kWeight>
-__device__ __forceinline__ float find_window(Lists& f, const Cluster::Four& slot, int own, int per, uint32_t top_k, float aim) {
+__device__ __forceinline__ float2 find_window(Lists& f, const Cluster::Four& slot, int own, int per, uint32_t top_k, float aim, bool spread) {
   const int lane = threadIdx.x & 31;
   auto reached = [&](uint32_t n, float e) { return kWeight ? e >= aim : n >= top_k; };
   uint32_t n = 0;
@@ -900,18 +902,21 @@ __device__ __forceinline__ float find_window(Lists& f, const Cluster::Four& slot
   cross_e = __shfl_sync(0xFFFFFFFFu, cross_e, l0);
   cross_w = __shfl_sync(0xFFFFFFFFu, cross_w, l0);
   in_cross = __shfl_sync(0xFFFFFFFFu, in_cross, l0);
-  // For top-k the window is the bin; for top-p, in a bin of few logits, the bins
-  // around it with kMargin logits on both sides, in a bin of many the steps
-  // around the place in it where the estimate puts the border.
+  // For top-k the window is the bin.  For top-p, in a bin of few logits, it is the
+  // bins around it with kMargin logits on both sides; in a bin of many the steps
+  // around the place in it where the estimate puts the border, or all of it where
+  // that is no good: bf16 logits, which lie on a few of its steps, and a second
+  // look.
   int c0 = 8 * cross, c1 = 8 * cross + 7;
-  float e_c0 = cross_e;
-  if (kWeight && in_cross > kMargin) {
+  float e_c0 = cross_e, e_c1 = cross_e + cross_w;
+  if (kWeight && in_cross > kMargin && spread) {
     const float place = fminf(fmaxf((aim - cross_e) / cross_w, 0.f), 1.f) * 8.f;
     const float reach = 8.f * kMargin / (float)in_cross + 0.25f;
     c0 += (int)floorf(place - reach);
     c1 = 8 * cross + (int)ceilf(place + reach);
     e_c0 += cross_w * (float)(c0 - 8 * cross) * 0.125f;
-  } else if (kWeight) {
+    e_c1 = cross_e + cross_w * (float)(c1 + 1 - 8 * cross) * 0.125f;
+  } else if (kWeight && in_cross <= kMargin) {
     n = n_first;
     e = e_first;
     for (int i = 0; i < bins; ++i) {
@@ -921,21 +926,27 @@ __device__ __forceinline__ float find_window(Lists& f, const Cluster::Four& slot
         c0 = min(c0, 8 * bin);
         e_c0 = fminf(e_c0, e);
       }
-      if (bin > cross && n + c <= cross_n + in_cross + kMargin) c1 = max(c1, 8 * bin + 7);
       n += c;
       e += bin_estimate(word, bin);
+      if (bin > cross && n <= cross_n + in_cross + kMargin) {
+        c1 = max(c1, 8 * bin + 7);
+        e_c1 = fmaxf(e_c1, e);
+      }
     }
     c0 = __reduce_min_sync(0xFFFFFFFFu, c0);
     c1 = __reduce_max_sync(0xFFFFFFFFu, c1);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) e_c0 = fminf(e_c0, __shfl_xor_sync(0xFFFFFFFFu, e_c0, o));
+    for (int o = 16; o > 0; o >>= 1) {
+      e_c0 = fminf(e_c0, __shfl_xor_sync(0xFFFFFFFFu, e_c0, o));
+      e_c1 = fmaxf(e_c1, __shfl_xor_sync(0xFFFFFFFFu, e_c1, o));
+    }
   }
   if (lane == 0) {
     f.c0 = c0;
     f.c1 = c1;
     f.before = cross_n;
   }
-  return e_c0;
+  return make_float2(e_c0, e_c1);
 }
 
 // kWeight false: the top_k-th largest of the logits >= base.  kWeight true: the
@@ -1021,7 +1032,8 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
     return out;  // the support holds no more
   // The border is where the running estimate (for top-k the running count,
   // which is exact) reaches the aim.  One warp looks up where.
-  float aim = 0.f, e_c0 = 0.f;
+  float aim = 0.f;
+  float2 around = {0.f, 0.f};
   if (kWeight && threadIdx.x < 32) {
     float e_all = 0.f;
 #pragma unroll
@@ -1035,7 +1047,7 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
   u64 over = 0;
   bool listed = false;  // what is in it is in f.cand
   for (int attempt = 0; attempt < kTries; ++attempt) {
-    if (threadIdx.x < 32) e_c0 = find_window<kWeight>(f, slot, own, per, (uint32_t)top_k, aim);
+    if (threadIdx.x < 32) around = find_window<kWeight>(f, slot, own, per, (uint32_t)top_k, aim, attempt == 0 && R::kKeyBits == 0);
     if (threadIdx.x == 0) f.count = 0;
     __syncthreads();
     const int c0 = f.c0, c1 = f.c1;
@@ -1092,35 +1104,38 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
       listed = cl.max((uint32_t)f.count) <= (uint32_t)kList;
       break;
     }
-    // the exact sums say by how much the estimate was off
+    // the exact sums say by how much the estimate was off, and on which side of
+    // the window to look
     const uint2 one = row.s->table[row.top_place & (kGrid - 1)];
     const float unit = (float)fixed(Weight{one.x + kMagicBits, row.rw.top - (row.top_place >> kGridBits)});
-    aim = fmaxf(e_c0 + (float)(long long)(need - over) / unit, 0.f);
+    aim = around.x + (float)(long long)(need - over) / unit;
+    aim = over < need ? fmaxf(aim, around.y * (1.f + 0x1p-22f)) : fmaxf(fminf(aim, around.x * (1.f - 0x1p-22f)), 0.f);
     over = 0;
   }
   // The largest key whose logits, up to `high`, hold what is needed (those of
   // `low` do), by quartering.
-  uint32_t from = key_of(low), to = key_of(high);
+  uint32_t from = key_of(low) >> R::kKeyBits, to = key_of(high) >> R::kKeyBits;
   while (from < to) {
     const uint32_t span = to - from;
     const uint32_t mid[3] = {from + span / 4 + 1, from + span / 2 + 1, from + span / 4 * 3 + 1};
+    const float least = key_float(mid[0] << R::kKeyBits);
     u64 c[3] = {0, 0, 0};
     if (listed) {
       for (int i = threadIdx.x; i < f.count; i += kThreads) {
         const uint32_t key = (uint32_t)(f.cand[i] >> 32);
         const u64 w = kWeight ? row.weight(key_float(key)) : 1;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) c[j] += key >= mid[j] ? w : 0;
+        for (int j = 0; j < 3; ++j) c[j] += key >> R::kKeyBits >= mid[j] ? w : 0;
       }
       __syncwarp();
     } else {
-      row.reaching(key_float(mid[0]), [&](const float(&x)[kN], int) {
+      row.reaching(least, [&](const float(&x)[kN], int) {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          if (x[i] >= key_float(mid[0]) && x[i] <= high) {
+          if (x[i] >= least && x[i] <= high) {
             const u64 w = kWeight ? row.weight(x[i]) : 1;
 #pragma unroll
-            for (int j = 0; j < 3; ++j) c[j] += x[i] >= key_float(mid[j]) ? w : 0;
+            for (int j = 0; j < 3; ++j) c[j] += x[i] >= key_float(mid[j] << R::kKeyBits) ? w : 0;
           }
       });
     }
@@ -1137,7 +1152,7 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
       to = mid[0] - 1;
     }
   }
-  out.x = key_float(from);
+  out.x = fmaxf(low, key_float(from << R::kKeyBits));
   return out;
 }
 
@@ -1402,11 +1417,16 @@ struct Shape {
 // CTAs a row.  More make a row's passes shorter, but its meetings dearer, and
 // two CTAs on an SM get in each other's way.  So: as many as leave every CTA an
 // SM of its own, of at least 4096 logits each; where every logit's weight is
-// needed (`heavy`: top-p over the vocabulary, or no filter) up to two CTAs an SM,
-// of at least 16384 logits.  In us with 1, 2, 4 and 8 CTAs a row of 163840 fp32
+// needed (`heavy`: top-p or a large top-k over the vocabulary, or no filter) up to
+// two CTAs an SM of 16384 logits, and in proportion more of longer ones, which
+// even out the last wave.  In us with 1, 2, 4 and 8 CTAs a row of 163840 fp32
 // logits:
 //   min-p, 1 row 14 10 8 7, 32 rows 15 10 8 9, 67 rows 15 10 11 17, 152 rows 19 18 27 36
-//   top-p 0.95 with probs, 32 rows 145 83 44 40, 64 rows 149 84 61 69
+//     160 rows 25 29 32, 512 rows 61 69 76
+//   no filter, 160 rows 72 63 57 68, 320 rows 114 99 96 124, 512 rows 149 135 144 193
+//   top-p 0.95, 100 rows 92 65 64 82, 256 rows 132 118 131 195, 700 rows 265 273 325 504
+//     with probs, 32 rows 145 83 44 40, 64 rows 149 84 61 69
+//   top-k 1000, 160 rows 126 118 99 121, 512 rows 266 259 241 351
 // and 67 mixed rows of 32003 bf16 33 21 26 37.  (Clusters of eight are placed two
 // CTAs to an SM long before the SMs run out: 16 rows under top-k 50 take 13.4 us
 // with eight CTAs a row, 11.0 with four.)  A slice that does not fit in shared
@@ -1419,7 +1439,8 @@ Shape row_shape(int T, int V, int elem, bool heavy) {
   auto alone = [&](int c) { return c <= 4 ? (long long)T * c <= kSms : T <= 12; };
   auto worth = [&](int c) {
     return (alone(c) && slice_of(c) >= 4096) ||
-           ((long long)T * c <= 2 * kSms && slice_of(c) >= (heavy ? 16384 : 65536));
+           (heavy ? slice_of(c) >= 16384 && (long long)T * c * 16384 <= 2ll * kSms * slice_of(c)
+                  : slice_of(c) >= 65536 && (long long)T * c <= 2 * kSms);
   };
   int c = 1;
   while (c < kClusterMax && worth(2 * c)) c *= 2;
@@ -1508,7 +1529,7 @@ extern "C" sv_status sample_tokens(const void* logits, int logits_type, int T, i
   const bool filters = top_k || top_k_all > 0 || top_p || top_p_all < 1.f;
   const bool small_k = !top_k && top_k_all > 0 && top_k_all <= kPublished / 2;
   const bool floored = min_p || min_p_all > 0.f || (!temperature && temperature_all < kColdest);
-  const Shape sh = row_shape(T, V, elem, filters ? (top_p || top_p_all < 1.f) && !small_k : !floored);
+  const Shape sh = row_shape(T, V, elem, filters ? (top_p || top_p_all < 1.f || (!top_k && top_k_all > 0)) && !small_k : !floored);
   a.slice = sh.slice;
   a.down = 0;
   while ((1 << a.down) < V) ++a.down;  // V <= 2^down: V (2^63 >> down) <= 2^63

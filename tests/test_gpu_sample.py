@@ -277,6 +277,17 @@ def test_crowded_borders(sv, kind, T):
         check(sv, x, u, s)
 
 
+@pytest.mark.parametrize("T,V", [(2, 163840), (40, 50001), (200, 30000)])
+@pytest.mark.parametrize("temperature", [0.3, 1.3])
+def test_borders_among_bf16_values(sv, T, V, temperature):
+    """bf16 logits lie on few values, hundreds on each, some on both sides of zero."""
+    rng = np.random.default_rng(T)
+    x = dev(logits(rng, T, V, peaks=24)).bfloat16()
+    u = rng.random(T).astype(np.float32)
+    for s in (dict(top_p=0.3), dict(top_p=0.8), dict(top_p=0.999), dict(top_k=V // 2, top_p=0.9), dict(top_k=V // 3)):
+        check(sv, x, u, dict(temperature=temperature) | s)
+
+
 def test_more_equal_than_candidates(sv):
     """A top-k whose last place is shared by more logits than can be ranked in
     one CTA: they are all kept."""
