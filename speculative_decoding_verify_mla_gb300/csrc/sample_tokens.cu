@@ -24,8 +24,8 @@
 //
 // One thread-block cluster per row.  With few rows a row has up to eight CTAs,
 // each with its slice in shared memory, so that the logits cross HBM once
-// whatever the filters need; with many rows it has one, which reads again (from
-// L2, mostly) what little it needs again.  The CTAs meet in distributed shared
+// whatever the filters need; with many rows it has one or a few, which read
+// again (from L2, mostly) what they need again.  The CTAs meet in distributed shared
 // memory.  How the thresholds are found:
 //  * A small top-k (the usual one): every warp publishes its largest logits;
 //    the k-th largest of those bounds the k-th largest of the row from below
@@ -754,6 +754,7 @@ __device__ __forceinline__ bool small_top_k(R& row, Lists& f, const SampleArgs& 
   if (mine[0] > kList) return false;
   const int n = (int)mine[0];
   if (a.probs || row.cl.rank == 0) {
+    if (threadIdx.x == 0) f.found = 0;  // no key: where fewer than top_k reach the bound (the support's end)
     row.bring(f, counts[0], false);
     const int per = threads_per(n), i = (int)threadIdx.x / per;
     const bool speaks = i < n && ((int)threadIdx.x & (per - 1)) == 0;
@@ -805,21 +806,6 @@ struct Border {
   bool ready;  // top-p: `here` is the thread's weight above the window, and f.cand holds what is in it
   u64 here;
 };
-
-__device__ __forceinline__ void smem_add(uint32_t addr, uint32_t v) {
-  asm volatile("red.shared.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-// Where x >= base: part onto sum, one onto the bin; without a branch.
-__device__ __forceinline__ void add_where_counted(float x, float base, u64 part, uint32_t bin, uint32_t one, u64& sum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ge.f32 p, %3, %4;\n\t"
-      "@p add.u64 %0, %0, %5;\n\t"
-      "@p red.shared.add.u32 [%1], %2;\n\t}"
-      : "+l"(sum)
-      : "r"(bin), "r"(one), "f"(x), "f"(base), "l"(part)
-      : "memory");
-}
 
 // Where the border is looked up: a window of grid steps [f.c0, f.c1] below the
 // largest logit.  aim: the estimate that it has to reach (top-p; top_k else); where
@@ -963,29 +949,29 @@ __device__ __forceinline__ Border find_border(R& row, Lists& f, float base, int 
   __syncthreads();
   // the histogram and, for top-p, the parts of all weights
   u64 all = 0;
-  const uint32_t hist = smem_u32(f.hist);
-  row.sl.template own<kResident, 8 / kN>([&](const float(&x)[kN], int, int) {
+  auto count_in = [&](const float(&x)[kN], int) {
     uint32_t bin[kN], one[kN];
-    u64 part[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       uint32_t k;
-      if (kWeight)
-        part[i] = part_of(weight_of(row.rw, row.s->table, x[i], &k));
-      else
+      if (kWeight) {
+        const u64 part = part_of(weight_of(row.rw, row.s->table, x[i], &k));
+        all += x[i] >= base ? part : 0;
+      } else {
         k = place_of(row.rw, x[i]);
+      }
       const uint32_t d = row.top_place - k;
-      bin[i] = hist + (d >> 3) * 4;
+      bin[i] = d >> 3;
       one[i] = ((d << kCountBits) & (7u << kCountBits)) | 1u;
     }
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (kWeight)
-        add_where_counted(x[i], base, part[i], bin[i], one[i], all);
-      else if (x[i] >= base)
-        smem_add(bin[i], one[i]);
-    }
-  });
+    for (int i = 0; i < kN; ++i)
+      if (x[i] >= base) atomicAdd(f.hist + bin[i], one[i]);
+  };
+  if constexpr (kWeight)
+    row.sl.template own<kResident, 8 / kN>([&](const float(&x)[kN], int i0, int) { count_in(x, i0); });
+  else
+    row.reaching(base, count_in);
   cl.sync();
   // CTA r adds up share r of the bins (from the largest weights down), thread i
   // of it `per` bins, so that the slots of a meeting are in bin order too.  The
@@ -1325,29 +1311,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   u64 total = 0, mine = 0;
   bool drawn = false, summed = false;
   if constexpr (kFilters) {
-    if (bound > -INFINITY) drawn = small_top_k(row, f, a, t, top_k, bound, top_p, chance, &theta, &total);
-    if (!drawn) {
-      float base = row.rw.least;
-      if (top_k > 0) {
+    // a small top-k, from the logits that reach the bound; where those are too
+    // many, or no bound is known, from the k-th largest logit on
+    float base = row.rw.least;
+#pragma unroll 1
+    for (int tries = bound > -INFINITY ? 0 : 1; top_k > 0 && tries < 2 && !drawn; ++tries) {
+      if (tries == 1) {
+        base = fmaxf(base, bound);
         base = fmaxf(base, find_border<false>(row, f, base, top_k, 0.f).x);
         theta = fmaxf(theta, base);
+        bound = base;
+        if (top_k > kList) break;
+        if (threadIdx.x == 0) f.count = 0;
+        cl.sync();  // nobody reads another's candidates any more
       }
-      if (top_p < 1.f) {
-        const Border b = find_border<true>(row, f, base, 0, top_p);
-        // where min-p cuts no further, the weight above the window and the
-        // warp's own among this CTA's candidates make up what it keeps
-        summed = b.ready && b.x >= theta;
-        theta = fmaxf(theta, b.x);
-        if (summed) {
-          mine = b.here;
-          const int from = warp * sl.run() * kN - sl.head, to = sl.run_end() * kN - sl.head;
-          for (int i = lane; i < f.count; i += 32) {
-            const float x = key_float((uint32_t)(f.cand[i] >> 32));
-            const int at = (int)(uint32_t)f.cand[i] - row.lo;
-            if (x >= theta && at >= from && at < to) mine += row.weight(x);
-          }
-          __syncwarp();
+      drawn = small_top_k(row, f, a, t, top_k, bound, top_p, chance, &theta, &total);
+    }
+    if (!drawn && top_p < 1.f) {
+      const Border b = find_border<true>(row, f, base, 0, top_p);
+      // where min-p cuts no further, the weight above the window and the
+      // warp's own among this CTA's candidates make up what it keeps
+      summed = b.ready && b.x >= theta;
+      theta = fmaxf(theta, b.x);
+      if (summed) {
+        mine = b.here;
+        const int from = warp * sl.run() * kN - sl.head, to = sl.run_end() * kN - sl.head;
+        for (int i = lane; i < f.count; i += 32) {
+          const float x = key_float((uint32_t)(f.cand[i] >> 32));
+          const int at = (int)(uint32_t)f.cand[i] - row.lo;
+          if (x >= theta && at >= from && at < to) mine += row.weight(x);
         }
+        __syncwarp();
       }
     }
   }

@@ -300,6 +300,25 @@ def test_more_equal_than_candidates(sv):
         assert np.all((run(sv, dev(x), rng.random(T).astype(np.float32), s)[1] > 0).sum(1) >= 1200)
 
 
+@pytest.mark.parametrize("T", [1, 30, 200])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_largest_side_by_side(sv, T, dtype):
+    """The largest logits in one stretch of the vocabulary, sorted, or falling
+    with the index, so that the parts of a row say little about its k-th largest;
+    and rows in which fewer logits than k have any weight."""
+    rng = np.random.default_rng(24)
+    V = 40003
+    x = rng.standard_normal((T, V)) * 2 - 0.0003 * np.arange(V)
+    x[0::3, 700:2700] += 9
+    x[1::3] = np.sort(x[1::3], axis=1)
+    if T > 1:
+        x[2, 40:] = -200.0
+    x = dev(x.astype(np.float32)).to(dtype)
+    u = rng.random(T).astype(np.float32)
+    for s in (dict(top_k=50, top_p=0.9), dict(top_k=250), dict(top_k=400, top_p=0.97), dict(top_k=512, min_p=0.01), dict(top_k=700, top_p=0.5)):
+        check(sv, x, u, s)
+
+
 def test_repeated_calls_agree(sv):
     """Nothing of a call is left for the next: calls of different shapes and
     settings in turn, on two streams at once, give each time the same bits."""
