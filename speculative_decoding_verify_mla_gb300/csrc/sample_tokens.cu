@@ -25,12 +25,13 @@
 // One thread-block cluster per row.  With few rows a row has up to eight CTAs,
 // each with its slice in shared memory, so that the logits cross HBM once
 // whatever the filters need; with many rows it has one or a few, which read
-// again (from L2, mostly) what they need again.  The CTAs meet in distributed shared
-// memory.  How the thresholds are found:
+// again (from L2, mostly) what they need again.  The CTAs meet in distributed
+// shared memory.  How the thresholds are found:
 //  * A small top-k (the usual one): every warp publishes its largest logits;
 //    the k-th largest of those bounds the k-th largest of the row from below
 //    and leaves about 1.4 k candidates, which one CTA ranks; top-p, min-p and
-//    the draw then look at the candidates alone.
+//    the draw then look at the candidates alone.  Where it leaves too many (the
+//    largest lie side by side) the k-th is found among them by counts first.
 //  * A large top-k, or top-p over the whole vocabulary: a histogram of counts
 //    over 1/64 octaves of weight.  Counts place the k-th logit's bin exactly;
 //    for top-p they place the border to within a fraction of a bin.  One more
